@@ -75,6 +75,13 @@ _sig("gc_grad_norm_noalloc", _i32, C.POINTER(gc_span), _i32, _i32, _vp, _vp)
 _sig("gc_passthrough", _i32, C.POINTER(gc_vec), _i32, _i32, _f32, _vp)
 _sig("gc_accordion_select", _i32, C.POINTER(C.c_float), C.POINTER(C.c_float), _i32, _f32, _i32,
      C.POINTER(C.c_int))
+_sig("gc_mxfp4_code_bytes", _sz, _i64, _i64)
+_sig("gc_mxfp4_scale_bytes", _sz, _i64, _i64)
+_sig("gc_mxfp4_ef_encode", _i32, _vp, _i32, _vp, _i64, _f32, _vp, _vp, _vp)
+_sig("gc_mxfp4_decode", _i32, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _f32, _vp, _i32, _i32, _vp)
+_sig("gc_mxfp4_quantize", _i32, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp)
+_sig("gc_mxfp4_matmul_workspace_bytes", _sz, _i64, _i64, _i64)
+_sig("gc_mxfp4_matmul", _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i32, _i32, _vp, _sz, _vp)
 _sig("gc_timing_enable", _i32, C.c_char_p)
 _sig("gc_timing_read", _i32, C.POINTER(C.c_double), C.POINTER(C.c_int64))
 _sig("gc_kernel_names", C.c_char_p)
@@ -86,6 +93,8 @@ EXPORTED = ["gc_status_str", "gc_last_error", "gc_topk_workspace_bytes", "gc_top
             "gc_powersgd_plan_bytes", "gc_powersgd_plan", "gc_powersgd_run", "gc_powersgd_run_phases",
             "gc_grad_norm_workspace_bytes", "gc_grad_norm", "gc_grad_norm_noalloc", "gc_passthrough",
             "gc_accordion_select",
+            "gc_mxfp4_code_bytes", "gc_mxfp4_scale_bytes", "gc_mxfp4_ef_encode", "gc_mxfp4_decode",
+            "gc_mxfp4_quantize", "gc_mxfp4_matmul_workspace_bytes", "gc_mxfp4_matmul",
             "gc_timing_enable", "gc_timing_read", "gc_kernel_names"]
 
 
@@ -467,6 +476,117 @@ def gc_accordion_select(norm_now, norm_prev, threshold: float, has_prev: bool):
                                    now.size, float(threshold), 1 if has_prev else 0,
                                    lv.ctypes.data_as(C.POINTER(C.c_int))), "gc_accordion_select")
     return lv, prev
+
+
+# ------------------------------------------------------------------ MXFP4
+
+def gc_mxfp4_code_bytes(rows: int, cols: int) -> int:
+    return int(lib.gc_mxfp4_code_bytes(rows, cols))
+
+
+def gc_mxfp4_scale_bytes(rows: int, cols: int) -> int:
+    return int(lib.gc_mxfp4_scale_bytes(rows, cols))
+
+
+def _mx_held(codes, scales, rows: int, cols: int, name: str):
+    """An MXFP4 matrix's two buffers: uint8, contiguous, with room for the shape."""
+    import torch
+    _dtype_is(codes, torch.uint8, f"{name} codes")
+    _dtype_is(scales, torch.uint8, f"{name} scales")
+    _need(codes.numel() >= lib.gc_mxfp4_code_bytes(rows, cols), f"{name} codes need gc_mxfp4_code_bytes entries")
+    _need(scales.numel() >= lib.gc_mxfp4_scale_bytes(rows, cols), f"{name} scales need gc_mxfp4_scale_bytes entries")
+
+
+def _pitched(t, name: str):
+    """(rows, cols, entries between rows) of a matrix whose rows are contiguous (a vector is one row)."""
+    _need(t.dim() in (1, 2) and t.numel() > 0, f"{name} must be a vector or a matrix with entries")
+    rows, cols = (1, t.shape[0]) if t.dim() == 1 else t.shape
+    _need(cols == 1 or t.stride(-1) == 1, f"{name} must have contiguous rows")
+    ld = cols if rows == 1 else t.stride(0)
+    _need(ld >= cols, f"{name} must have rows that do not overlap")
+    return rows, cols, ld
+
+
+def _same_device(first, *others):
+    if not first.is_cuda:
+        raise ValueError("expected a device tensor")
+    _need(all(t is None or t.device == first.device for t in others), "every tensor must be on the same device")
+
+
+def _enqueue(t, stream, where: str, fn, *args):
+    """Calls fn(*args, stream) with t's device current, on the given stream or that device's current one."""
+    import torch
+    if t.device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, _stream(stream)), where)
+
+
+def gc_mxfp4_ef_encode(grad, mem, eta: float, codes, scales, stream=None) -> None:
+    """MXFP4 step with memory: (codes, scales) <- Q(mem + eta*grad), mem <- what the message leaves out."""
+    import torch
+    _dtype_is(mem, torch.float32, "mem")
+    _need(grad.numel() == mem.numel() >= 1, "grad and mem must have the same number of entries, at least one")
+    d = mem.numel()
+    _mx_held(codes, scales, 1, d, "message")
+    _same_device(mem, grad, codes, scales)
+    _enqueue(mem, stream, "gc_mxfp4_ef_encode", lib.gc_mxfp4_ef_encode, _ptr(grad), _dtype_code(grad), _ptr(mem), d,
+             float(eta), _ptr(codes), _ptr(scales))
+
+
+def gc_mxfp4_decode(codes, scales, out, weight: float = 1.0, accumulate: bool = False, stream=None) -> None:
+    """out = [out +] weight * the sum of the messages' values.  out: a vector, or
+    a matrix (dense).  codes and scales: one message (1-D), or one a row (2-D, as
+    an all-gather leaves them; the rows may be further apart than their length)."""
+    import torch
+    _need(out.dim() in (1, 2) and out.numel() > 0, "out must be a vector or a matrix with entries")
+    rows, cols = (1, out.shape[0]) if out.dim() == 1 else out.shape
+    _dtype_is(codes, torch.uint8, "codes")
+    _dtype_is(scales, torch.uint8, "scales")
+    _need(codes.dim() == scales.dim() and codes.dim() in (1, 2), "codes and scales must both be 1-D or 2-D")
+    nmsg = 1 if codes.dim() == 1 else codes.shape[0]
+    _need(nmsg >= 1 and (scales.dim() == 1 or scales.shape[0] == nmsg), "codes and scales need one row per message")
+    _need(codes.shape[-1] >= lib.gc_mxfp4_code_bytes(rows, cols), "codes need gc_mxfp4_code_bytes entries a message")
+    _need(scales.shape[-1] >= lib.gc_mxfp4_scale_bytes(rows, cols), "scales need gc_mxfp4_scale_bytes entries a message")
+    _need(codes.stride(-1) == 1 and scales.stride(-1) == 1, "a message must be contiguous")
+    cs, ss = (codes.stride(0), scales.stride(0)) if nmsg > 1 else (0, 0)
+    _same_device(out, codes, scales)
+    _enqueue(out, stream, "gc_mxfp4_decode", lib.gc_mxfp4_decode, codes.data_ptr(), scales.data_ptr(), nmsg, cs, ss,
+             rows, cols, float(weight), _ptr(out), _dtype_code(out), 1 if accumulate else 0)
+
+
+def gc_mxfp4_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, stream=None) -> None:
+    """Q of a matrix along its rows (codes, scales: rows x cols), along its columns
+    (codes_t, scales_t: cols x rows, transposed), or both.  x may be a view with a row pitch."""
+    rows, cols, ld = _pitched(x, "x")
+    _need((codes is None) == (scales is None) and (codes_t is None) == (scales_t is None), "a form needs codes and scales")
+    _need(codes is not None or codes_t is not None, "no output given")
+    if codes is not None:
+        _mx_held(codes, scales, rows, cols, "row")
+    if codes_t is not None:
+        _mx_held(codes_t, scales_t, cols, rows, "column")
+    _same_device(x, codes, scales, codes_t, scales_t)
+    _enqueue(x, stream, "gc_mxfp4_quantize", lib.gc_mxfp4_quantize, x.data_ptr(), _dtype_code(x), rows, cols, ld,
+             _ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t))
+
+
+def gc_mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(lib.gc_mxfp4_matmul_workspace_bytes(m, n, k))
+
+
+def gc_mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, k: int, out, ws=None, accumulate: bool = False,
+                    stream=None) -> None:
+    """out [m, n] = [out +] A B^T for MXFP4 matrices A (m x k) and B (n x k); out may be a view with a row pitch."""
+    m, n, ldo = _pitched(out, "out")
+    k = int(k)
+    _need(k >= 1, "k must be at least 1")
+    _mx_held(a_codes, a_scales, m, k, "A")
+    _mx_held(b_codes, b_scales, n, k, "B")
+    _same_device(out, a_codes, a_scales, b_codes, b_scales, ws)
+    _enqueue(out, stream, "gc_mxfp4_matmul", lib.gc_mxfp4_matmul, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
+             _ptr(b_scales), m, n, k, out.data_ptr(), ldo, _dtype_code(out), 1 if accumulate else 0, _ptr(ws),
+             0 if ws is None else _nbytes(ws))
 
 
 # ------------------------------------------------------------------ timing hooks

@@ -1,0 +1,36 @@
+// What the MXFP4 sources share: the layout of a matrix and its scales.
+#pragma once
+
+#include "gc_common.h"
+
+namespace gc {
+
+constexpr int64_t MX_MAX_ENTRIES = int64_t(1) << 34;   // entries of one matrix, padded columns included
+
+// A row is held in groups of 128 columns: 64 bytes of codes, 4 scale bytes.
+inline int64_t mx_groups(int64_t cols) { return (cols + 127) / 128; }
+inline int64_t mx_code_bytes(int64_t rows, int64_t cols) { return rows * mx_groups(cols) * 64; }
+inline int64_t mx_scale_bytes(int64_t rows, int64_t cols) { return rows * mx_groups(cols) * 4; }
+inline bool mx_shape_ok(int64_t rows, int64_t cols) {
+    return rows >= 1 && cols >= 1 && cols <= MX_MAX_ENTRIES && rows <= MX_MAX_ENTRIES / (mx_groups(cols) * 128);
+}
+
+constexpr int64_t MX_MAX_DIM = (int64_t(1) << 30);      // rows, columns or depth of a product
+
+int mx_check_matrix(const char* fn, const char* name, const void* codes, const void* scales);
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// 2^(s - 127): a subnormal for s = 0, NaN for s = 255
+__device__ __forceinline__ float scale_value(unsigned s) {
+    return __uint_as_float(s == 255u ? 0x7FC00000u : s ? s << 23 : 0x00400000u);
+}
+
+// Two float32 as packed bf16 (round to nearest even), the first in the low half.
+__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 r = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(unsigned, r);
+}
+
+}  // namespace gc

@@ -318,6 +318,94 @@ typedef struct gc_vec {
 int gc_passthrough(const gc_vec* vecs, int nvecs, int grad_dtype, float eta, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* MXFP4: microscaled 4-bit floating point                                  */
+/* ------------------------------------------------------------------------ */
+
+/* An MXFP4 matrix of rows x cols entries (a vector is one row) is two device
+ * buffers.  Each row is held in G = ceil(cols / 128) groups of 128 columns:
+ *   codes   rows x 64 G bytes: E2M1 codes, two a byte, the lower column in the
+ *           low four bits (sign, two exponent bits, one mantissa bit: the
+ *           magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 in code order);
+ *   scales  rows x 4 G bytes: one E8M0 byte s per 32 columns, standing for
+ *           2^(s - 127); 255 is NaN, and every value of its block is NaN.
+ * Columns past cols have code 0, blocks without a column the byte 0: every
+ * call that writes a matrix writes them so, and gc_mxfp4_matmul takes them so.
+ * A message of gc_mxfp4_ef_encode for an n x m gradient with m % 128 == 0 is
+ * byte for byte the MXFP4 matrix n x m.
+ *
+ * Quantising a block (Q below): with E the biased float32 exponent of its
+ * largest magnitude, s = max(E - 2, 0); a code is entry * 2^(127 - s) rounded
+ * to the nearest E2M1 magnitude (ties to the even code), at most 6, with the
+ * entry's sign.  A block with an entry that is not finite gets s = 255 and
+ * zero codes.  D below gives back the values, exactly, in float32 (a value
+ * past its range, from a scale byte that no call here writes, is infinite). */
+
+/* Bytes of the two buffers; 0 when the shape is out of range: rows, cols >= 1
+ * and rows * 128 G <= 2^34. */
+size_t gc_mxfp4_code_bytes(int64_t rows, int64_t cols);
+size_t gc_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+/* One error-feedback step with the quantiser as the compressor, in the memory
+ * convention of the steps above ("Sparsified SGD with Memory", method section):
+ *     acc = fl32(mem + fl32(eta * grad))      (as in gc_topk_ef_encode)
+ *     (codes, scales) = Q(acc);  mem = fl32(acc - D(codes, scales))
+ *   grad    [d] float32 or bf16 (grad_dtype), read only
+ *   mem     [d] float32, in/out
+ *   d       1 <= d <= 2^34
+ *   codes   [gc_mxfp4_code_bytes(1, d)] out;  scales [gc_mxfp4_scale_bytes(1, d)] out
+ * No workspace.  An entry of acc that is not finite turns its block's values
+ * into NaN, in the message and in mem: a caller that skips overflowed steps
+ * checks the gradient first (gc_grad_norm).
+ * Errors: GC_ERR_ARG (null pointer, d out of range, misalignment, overlapping
+ * buffers), GC_ERR_DTYPE, GC_ERR_HIP. */
+int gc_mxfp4_ef_encode(const void* grad, int grad_dtype, float* mem, int64_t d, float eta, uint8_t* codes,
+                       uint8_t* scales, void* stream);
+
+/* Decode of nmsg >= 1 messages of the same shape, as an all-gather leaves them:
+ *     out = [out +] fl32(weight * sum_i D(message i))
+ * The sum is taken in float32 in message order; out [rows x cols], dense, is
+ * float32 or bf16 (out_dtype; one rounding at the end).  accumulate != 0 adds
+ * to out's old values.  Message i starts at codes + i * code_stride and
+ * scales + i * scale_stride (bytes; multiples of 16 and 4, at least a message
+ * and at most 2^40; not read for nmsg == 1).
+ * Errors: GC_ERR_ARG (null or misaligned pointer, shape, nmsg or strides out
+ * of range, out overlapping a message), GC_ERR_DTYPE, GC_ERR_HIP. */
+int gc_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int nmsg, int64_t code_stride, int64_t scale_stride,
+                    int64_t rows, int64_t cols, float weight, void* out, int out_dtype, int accumulate, void* stream);
+
+/* Quantisation of a matrix x [rows x cols], rows ld entries apart (ld >= cols),
+ * float32 or bf16, without memory: the operands of gc_mxfp4_matmul.
+ *   codes, scales      Q along the rows: the MXFP4 matrix rows x cols, or both NULL
+ *   codes_t, scales_t  Q along the columns, transposed: the MXFP4 matrix
+ *                      cols x rows, or both NULL
+ * With both forms asked for, x is read once.  For y = x W^T the forward product
+ * takes x and W by rows; the gradients dx = dy W and dW = dy^T x take dy by
+ * rows with W by columns, and dy and x by columns.
+ * Errors: GC_ERR_ARG (null or misaligned pointer, no form asked for, half a
+ * form, shape or ld out of range, overlapping buffers), GC_ERR_DTYPE, GC_ERR_HIP. */
+int gc_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                      uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, void* stream);
+
+/* Workspace bytes of gc_mxfp4_matmul (0: none is needed, or a size is out of range). */
+size_t gc_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/* Product of two MXFP4 matrices, both with the summed index along their rows:
+ *     out[i, j] = [out[i, j] +] sum_k D(A)[i, k] * D(B)[j, k]
+ * A is m x k, B is n x k; out has m rows of n entries, ldo entries apart
+ * (ldo >= n), float32 or bf16 (out_dtype).  Products are summed in float32 in
+ * an order fixed by the sizes; out is rounded once.  Entries of out between
+ * the rows (n .. ldo) are left alone.
+ *   m, n, k  in [1, 2^30], each matrix within the range above, m x n too
+ *   ws       >= gc_mxfp4_matmul_workspace_bytes(m, n, k) bytes (may be NULL for 0)
+ * out is what the compressors take as a gradient: with A = dy and B = x by
+ * columns it is dW, and accumulate != 0 adds up micro-batches.
+ * Errors: GC_ERR_ARG (null or misaligned pointer, size or ldo out of range, out
+ * or ws overlapping a buffer), GC_ERR_DTYPE, GC_ERR_WORKSPACE, GC_ERR_HIP. */
+int gc_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
+                    int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype, int accumulate, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Accordion: per-layer norms and the l_low / l_high switch                 */
 /* ------------------------------------------------------------------------ */
 
