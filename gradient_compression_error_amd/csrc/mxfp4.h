@@ -15,7 +15,8 @@ inline bool mx_shape_ok(int64_t rows, int64_t cols) {
     return rows >= 1 && cols >= 1 && cols <= MX_MAX_ENTRIES && rows <= MX_MAX_ENTRIES / (mx_groups(cols) * 128);
 }
 
-constexpr int64_t MX_MAX_DIM = (int64_t(1) << 30);      // rows, columns or depth of a product
+constexpr int64_t MX_MAX_DIM = int64_t(1) << 30;       // rows or columns of a product
+constexpr int64_t MX_MAX_K = int64_t(1) << 24;         // its depth: 256 rows of codes stay within 32-bit offsets
 
 int mx_check_matrix(const char* fn, const char* name, const void* codes, const void* scales);
 

@@ -395,7 +395,8 @@ size_t gc_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
  * (ldo >= n), float32 or bf16 (out_dtype).  Products are summed in float32 in
  * an order fixed by the sizes; out is rounded once.  Entries of out between
  * the rows (n .. ldo) are left alone.
- *   m, n, k  in [1, 2^30], each matrix within the range above, m x n too
+ *   m, n     in [1, 2^30], k in [1, 2^24]; each matrix, and m x n, within the
+ *            range above
  *   ws       >= gc_mxfp4_matmul_workspace_bytes(m, n, k) bytes (may be NULL for 0)
  * out is what the compressors take as a gradient: with A = dy and B = x by
  * columns it is dW, and accumulate != 0 adds up micro-batches.
