@@ -294,6 +294,29 @@ def test_product_exact(m, n, k):
     assert torch.equal(half, (torch.from_numpy(want).float() + old16.float()).to(torch.bfloat16))
 
 
+# the kernels for larger outs: few rows of many columns, one and several parts of k, both tile sizes at few and many groups
+LARGE_PRODUCTS = [(1, 20000, 300), (16, 9000, 1000), (30, 9000, 200), (500, 1000, 1000), (777, 1001, 1155), (1100, 1500, 1500),
+                  (300, 520, 16384), (601, 1001, 20000), (1500, 1100, 16400), (2100, 2001, 100), (2100, 2001, 130),
+                  (2050, 2100, 700), (2100, 2000, 1000), (4000, 3970, 384), (4000, 4001, 400), (4001, 3900, 520),
+                  (4000, 3970, 700), (3900, 4000, 900), (3841, 4095, 1155), (8000, 8000, 200)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE_PRODUCTS)
+def test_large_product_exact(m, n, k):
+    """As above (K < 2^14.8: 36 * 16 * K < 2^24)."""
+    print(f"case: mxfp4 matmul exact {m}x{n}x{k}", flush=True)
+    r = gen.rng(0, gen.KIND_MISC, 507, m * 31 + n * 7 + k)
+    a, b = random_held(r, m, k, 126, 127), random_held(r, n, k, 126, 127)
+    want = torch.from_numpy(oracle.mxfp4_matmul(a, b, k).astype(np.float32))
+    old = torch.from_numpy(r.integers(-1000, 1000, (m, n)).astype(np.float32) / np.float32(16))
+    assert torch.equal(product(a, b, m, n, k, old=old.numpy(), pitch=n + n % 2), want + old)
+    assert torch.equal(product(a, b, m, n, k), want)
+    assert torch.equal(product(a, b, m, n, k, dtype=torch.bfloat16, pitch=n + 8), want.to(torch.bfloat16))
+    old16 = old.to(torch.bfloat16)
+    got = product(a, b, m, n, k, dtype=torch.bfloat16, old=old16.float().numpy(), pitch=-(-n // 8) * 8)
+    assert torch.equal(got, (want + old16.float()).to(torch.bfloat16))
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 300, 1000), (16, 1024, 4096), (100, 130, 8192), (300, 260, 1155), (600, 1024, 16384)])
 def test_product_bound(m, n, k):
     """Scales over 24 binades, so that the sums round."""
@@ -347,7 +370,7 @@ def test_products_repeat_bitwise():
     gc = lib()
     print("case: mxfp4 matmul determinism", flush=True)
     r = gen.rng(0, gen.KIND_MISC, 504)
-    for m, n, k in [(4, 1024, 8192), (256, 512, 16384), (300, 700, 5000)]:
+    for m, n, k in [(4, 1024, 8192), (256, 512, 16384), (300, 700, 5000), (2100, 2000, 500), (4000, 3970, 384)]:
         a, b = held_from(*random_held(r, m, k, 100, 140)), held_from(*random_held(r, n, k, 100, 140))
         ws = torch.empty(max(16, gc.gc_mxfp4_matmul_workspace_bytes(m, n, k)), dtype=torch.uint8, device=DEV)
         outs = []
@@ -360,7 +383,8 @@ def test_products_repeat_bitwise():
 
 def test_workspace_too_small():
     gc = lib()
-    shapes = [(m, n, k) for m, n, k in PRODUCTS if gc.gc_mxfp4_matmul_workspace_bytes(m, n, k) > 0]
+    shapes = [(m, n, k) for m, n, k in LARGE_PRODUCTS if gc.gc_mxfp4_matmul_workspace_bytes(m, n, k) > 0]
+    assert shapes
     for m, n, k in shapes:
         r = gen.rng(0, gen.KIND_MISC, 505)
         a, b = held_from(*random_held(r, m, k, 127, 127)), held_from(*random_held(r, n, k, 127, 127))
@@ -368,7 +392,10 @@ def test_workspace_too_small():
         need = gc.gc_mxfp4_matmul_workspace_bytes(m, n, k)
         with pytest.raises(gc.GCError) as e:
             gc.gc_mxfp4_matmul(*a, *b, k, out, torch.empty(need - 16, dtype=torch.uint8, device=DEV))
-        assert e.value.status == gc.GC_ERR_WORKSPACE and bool((out == 3.0).all())
+        assert e.value.status == gc.GC_ERR_WORKSPACE
+        with pytest.raises(gc.GCError) as e:
+            gc.gc_mxfp4_matmul(*a, *b, k, out)
+        assert e.value.status == gc.GC_ERR_ARG and bool((out == 3.0).all())
 
 
 # ---------------------------------------------------------------- together, as they are used
