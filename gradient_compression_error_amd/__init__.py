@@ -488,87 +488,142 @@ def gc_mxfp4_scale_bytes(rows: int, cols: int) -> int:
     return int(lib.gc_mxfp4_scale_bytes(rows, cols))
 
 
-def _mx_held(codes, scales, rows: int, cols: int, name: str):
-    """An MXFP4 matrix's two buffers: uint8, contiguous, with room for the shape."""
-    import torch
-    _dtype_is(codes, torch.uint8, f"{name} codes")
-    _dtype_is(scales, torch.uint8, f"{name} scales")
-    _need(codes.numel() >= lib.gc_mxfp4_code_bytes(rows, cols), f"{name} codes need gc_mxfp4_code_bytes entries")
-    _need(scales.numel() >= lib.gc_mxfp4_scale_bytes(rows, cols), f"{name} scales need gc_mxfp4_scale_bytes entries")
+# Small calls are bound by the host, so these wrappers check in plain ifs (no
+# message is formed unless it is raised) and take the stream's handle directly.
+_torch = None
 
 
-def _pitched(t, name: str):
+def _mx_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _mx_held(torch, codes, scales, rows: int, cols: int, name: str):
+    """An MXFP4 matrix's two buffers: uint8, with room for the shape."""
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise TypeError(f"{name} codes and scales: expected torch.uint8, got {codes.dtype} and {scales.dtype}")
+    units = rows * ((cols + 127) >> 7)
+    if codes.numel() < 64 * units:
+        raise ValueError(f"{name} codes need gc_mxfp4_code_bytes entries")
+    if scales.numel() < 4 * units:
+        raise ValueError(f"{name} scales need gc_mxfp4_scale_bytes entries")
+
+
+def _mx_pitched(t, name: str):
     """(rows, cols, entries between rows) of a matrix whose rows are contiguous (a vector is one row)."""
-    _need(t.dim() in (1, 2) and t.numel() > 0, f"{name} must be a vector or a matrix with entries")
-    rows, cols = (1, t.shape[0]) if t.dim() == 1 else t.shape
-    _need(cols == 1 or t.stride(-1) == 1, f"{name} must have contiguous rows")
-    ld = cols if rows == 1 else t.stride(0)
-    _need(ld >= cols, f"{name} must have rows that do not overlap")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 1:
+        rows, cols, ld = 1, shape[0], shape[0]
+    elif len(shape) == 2:
+        rows, cols = shape
+        ld = cols if rows == 1 else stride[0]
+    else:
+        rows = cols = ld = 0
+    if rows < 1 or cols < 1:
+        raise ValueError(f"{name} must be a vector or a matrix with entries")
+    if cols > 1 and stride[-1] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if ld < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
     return rows, cols, ld
 
 
-def _same_device(first, *others):
-    if not first.is_cuda:
+def _mx_device(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("expected a device tensor")
-    _need(all(t is None or t.device == first.device for t in others), "every tensor must be on the same device")
+    return dev
 
 
-def _enqueue(t, stream, where: str, fn, *args):
-    """Calls fn(*args, stream) with t's device current, on the given stream or that device's current one."""
-    import torch
-    if t.device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
+def _mx_ptr(t, dev: int, contiguous: bool = True):
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("expected a device tensor" if t.get_device() < 0 else "every tensor must be on the same device")
+    if contiguous and not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _mx_call(torch, dev: int, stream, where: str, fn, *args) -> None:
+    """fn(*args, stream) with device dev current, on the given stream or that device's current one."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, stream)
     else:
-        with torch.cuda.device(t.device):
-            _check(fn(*args, _stream(stream)), where)
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc:
+        raise GCError(rc, where)
 
 
 def gc_mxfp4_ef_encode(grad, mem, eta: float, codes, scales, stream=None) -> None:
     """MXFP4 step with memory: (codes, scales) <- Q(mem + eta*grad), mem <- what the message leaves out."""
-    import torch
-    _dtype_is(mem, torch.float32, "mem")
-    _need(grad.numel() == mem.numel() >= 1, "grad and mem must have the same number of entries, at least one")
+    torch = _mx_torch()
+    if mem.dtype is not torch.float32:
+        raise TypeError(f"mem: expected torch.float32, got {mem.dtype}")
     d = mem.numel()
-    _mx_held(codes, scales, 1, d, "message")
-    _same_device(mem, grad, codes, scales)
-    _enqueue(mem, stream, "gc_mxfp4_ef_encode", lib.gc_mxfp4_ef_encode, _ptr(grad), _dtype_code(grad), _ptr(mem), d,
-             float(eta), _ptr(codes), _ptr(scales))
+    if d < 1 or grad.numel() != d:
+        raise ValueError("grad and mem must have the same number of entries, at least one")
+    _mx_held(torch, codes, scales, 1, d, "message")
+    dev = _mx_device(mem)
+    _mx_call(torch, dev, stream, "gc_mxfp4_ef_encode", lib.gc_mxfp4_ef_encode, _mx_ptr(grad, dev), _dtype_code(grad),
+             _mx_ptr(mem, dev), d, float(eta), _mx_ptr(codes, dev), _mx_ptr(scales, dev))
 
 
 def gc_mxfp4_decode(codes, scales, out, weight: float = 1.0, accumulate: bool = False, stream=None) -> None:
     """out = [out +] weight * the sum of the messages' values.  out: a vector, or
     a matrix (dense).  codes and scales: one message (1-D), or one a row (2-D, as
     an all-gather leaves them; the rows may be further apart than their length)."""
-    import torch
-    _need(out.dim() in (1, 2) and out.numel() > 0, "out must be a vector or a matrix with entries")
-    rows, cols = (1, out.shape[0]) if out.dim() == 1 else out.shape
-    _dtype_is(codes, torch.uint8, "codes")
-    _dtype_is(scales, torch.uint8, "scales")
-    _need(codes.dim() == scales.dim() and codes.dim() in (1, 2), "codes and scales must both be 1-D or 2-D")
-    nmsg = 1 if codes.dim() == 1 else codes.shape[0]
-    _need(nmsg >= 1 and (scales.dim() == 1 or scales.shape[0] == nmsg), "codes and scales need one row per message")
-    _need(codes.shape[-1] >= lib.gc_mxfp4_code_bytes(rows, cols), "codes need gc_mxfp4_code_bytes entries a message")
-    _need(scales.shape[-1] >= lib.gc_mxfp4_scale_bytes(rows, cols), "scales need gc_mxfp4_scale_bytes entries a message")
-    _need(codes.stride(-1) == 1 and scales.stride(-1) == 1, "a message must be contiguous")
+    torch = _mx_torch()
+    shape = out.shape
+    if len(shape) not in (1, 2) or out.numel() < 1:
+        raise ValueError("out must be a vector or a matrix with entries")
+    rows, cols = (1, shape[0]) if len(shape) == 1 else shape
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise TypeError(f"codes and scales: expected torch.uint8, got {codes.dtype} and {scales.dtype}")
+    nc, ns = codes.shape, scales.shape
+    if len(nc) != len(ns) or len(nc) not in (1, 2):
+        raise ValueError("codes and scales must both be 1-D or 2-D")
+    nmsg = 1 if len(nc) == 1 else nc[0]
+    if nmsg < 1 or (len(ns) == 2 and ns[0] != nmsg):
+        raise ValueError("codes and scales need one row per message")
+    units = rows * ((cols + 127) >> 7)
+    if nc[-1] < 64 * units:
+        raise ValueError("codes need gc_mxfp4_code_bytes entries a message")
+    if ns[-1] < 4 * units:
+        raise ValueError("scales need gc_mxfp4_scale_bytes entries a message")
+    if codes.stride(-1) != 1 or scales.stride(-1) != 1:
+        raise ValueError("a message must be contiguous")
     cs, ss = (codes.stride(0), scales.stride(0)) if nmsg > 1 else (0, 0)
-    _same_device(out, codes, scales)
-    _enqueue(out, stream, "gc_mxfp4_decode", lib.gc_mxfp4_decode, codes.data_ptr(), scales.data_ptr(), nmsg, cs, ss,
-             rows, cols, float(weight), _ptr(out), _dtype_code(out), 1 if accumulate else 0)
+    dev = _mx_device(out)
+    _mx_call(torch, dev, stream, "gc_mxfp4_decode", lib.gc_mxfp4_decode, _mx_ptr(codes, dev, False),
+             _mx_ptr(scales, dev, False), nmsg, cs, ss, rows, cols, float(weight), _mx_ptr(out, dev), _dtype_code(out),
+             1 if accumulate else 0)
 
 
 def gc_mxfp4_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, stream=None) -> None:
     """Q of a matrix along its rows (codes, scales: rows x cols), along its columns
     (codes_t, scales_t: cols x rows, transposed), or both.  x may be a view with a row pitch."""
-    rows, cols, ld = _pitched(x, "x")
-    _need((codes is None) == (scales is None) and (codes_t is None) == (scales_t is None), "a form needs codes and scales")
-    _need(codes is not None or codes_t is not None, "no output given")
+    torch = _mx_torch()
+    rows, cols, ld = _mx_pitched(x, "x")
+    if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
+        raise ValueError("a form needs codes and scales")
+    if codes is None and codes_t is None:
+        raise ValueError("no output given")
     if codes is not None:
-        _mx_held(codes, scales, rows, cols, "row")
+        _mx_held(torch, codes, scales, rows, cols, "row")
     if codes_t is not None:
-        _mx_held(codes_t, scales_t, cols, rows, "column")
-    _same_device(x, codes, scales, codes_t, scales_t)
-    _enqueue(x, stream, "gc_mxfp4_quantize", lib.gc_mxfp4_quantize, x.data_ptr(), _dtype_code(x), rows, cols, ld,
-             _ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t))
+        _mx_held(torch, codes_t, scales_t, cols, rows, "column")
+    dev = _mx_device(x)
+    _mx_call(torch, dev, stream, "gc_mxfp4_quantize", lib.gc_mxfp4_quantize, x.data_ptr(), _dtype_code(x), rows, cols, ld,
+             _mx_ptr(codes, dev), _mx_ptr(scales, dev), _mx_ptr(codes_t, dev), _mx_ptr(scales_t, dev))
 
 
 def gc_mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -578,15 +633,17 @@ def gc_mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
 def gc_mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, k: int, out, ws=None, accumulate: bool = False,
                     stream=None) -> None:
     """out [m, n] = [out +] A B^T for MXFP4 matrices A (m x k) and B (n x k); out may be a view with a row pitch."""
-    m, n, ldo = _pitched(out, "out")
+    torch = _mx_torch()
+    m, n, ldo = _mx_pitched(out, "out")
     k = int(k)
-    _need(k >= 1, "k must be at least 1")
-    _mx_held(a_codes, a_scales, m, k, "A")
-    _mx_held(b_codes, b_scales, n, k, "B")
-    _same_device(out, a_codes, a_scales, b_codes, b_scales, ws)
-    _enqueue(out, stream, "gc_mxfp4_matmul", lib.gc_mxfp4_matmul, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
-             _ptr(b_scales), m, n, k, out.data_ptr(), ldo, _dtype_code(out), 1 if accumulate else 0, _ptr(ws),
-             0 if ws is None else _nbytes(ws))
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    _mx_held(torch, a_codes, a_scales, m, k, "A")
+    _mx_held(torch, b_codes, b_scales, n, k, "B")
+    dev = _mx_device(out)
+    _mx_call(torch, dev, stream, "gc_mxfp4_matmul", lib.gc_mxfp4_matmul, _mx_ptr(a_codes, dev), _mx_ptr(a_scales, dev),
+             _mx_ptr(b_codes, dev), _mx_ptr(b_scales, dev), m, n, k, out.data_ptr(), ldo, _dtype_code(out),
+             1 if accumulate else 0, _mx_ptr(ws, dev), 0 if ws is None else ws.nbytes)
 
 
 # ------------------------------------------------------------------ timing hooks
