@@ -122,7 +122,7 @@ const char* gc_kernel_names(void) {
            "topk_count,topk_emit,topk_materialize,topk_decode_set,topk_decode_add,topk_small,randk_encode,"
            "psgd_pq,psgd_p,psgd_q,psgd_qreduce,psgd_out,psgd_decode,psgd_materialize,"
            "norm_partial,norm_final,passthrough,"
-           "mxfp4_rows,mxfp4_cols,mxfp4_decode,mxfp4_wave,mxfp4_tile,mxfp4_join";
+           "mxfp4_ef,mxfp4_rows,mxfp4_cols,mxfp4_decode,mxfp4_wave,mxfp4_tile,mxfp4_join";
 }
 
 }  // extern "C"

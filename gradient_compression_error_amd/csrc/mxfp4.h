@@ -22,16 +22,24 @@ int mx_check_matrix(const char* fn, const char* name, const void* codes, const v
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// 2^(s - 127): a subnormal for s = 0, NaN for s = 255
-__device__ __forceinline__ float scale_value(unsigned s) {
-    return __uint_as_float(s == 255u ? 0x7FC00000u : s ? s << 23 : 0x00400000u);
-}
+// Rows may start anywhere: vector accesses that need the alignment of an entry only.
+typedef unsigned u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Two float32 as packed bf16 (round to nearest even), the first in the low half.
 __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     const bf16x2 r = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
     return __builtin_bit_cast(unsigned, r);
+}
+
+// Workgroups b, b + 8, ... run on one XCD: gives XCD x the x-th stretch of the work
+// in order, so that its L2 serves what neighbours share.
+__device__ __forceinline__ unsigned xcd_place(unsigned b, unsigned count) {
+    const unsigned per = count / 8, more = count % 8, x = b % 8;
+    return x * per + min(x, more) + b / 8;
 }
 
 }  // namespace gc

@@ -44,22 +44,15 @@ struct Operand {
     int rows;
 };
 
-// Workgroups b, b + 8, ... run on one XCD: gives XCD x the x-th stretch of the work
-// in order, so that its L2 serves what neighbours share.
-__device__ __forceinline__ unsigned xcd_place(unsigned b, unsigned count) {
-    const unsigned per = count / 8, more = count % 8, x = b % 8;
-    return x * per + min(x, more) + b / 8;
-}
-
 // Sixteen bytes of a row of out, past the caches' replacement order: a tile is
 // written (and, when adding, read) once, and what the L2 holds of the operands is
 // worth more (8192^3 to bf16: 278 us with plain stores, 261 us with these).
 template <bool BF16>
-__device__ __forceinline__ u32x4 load16(const void* out, long long at) {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(out) + at * (BF16 ? 2 : 4)));
+__device__ __forceinline__ u32x4_any load16(const void* out, long long at) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(reinterpret_cast<const char*>(out) + at * (BF16 ? 2 : 4)));
 }
 template <bool BF16, int N>
-__device__ __forceinline__ void add16(float (&v)[N], u32x4 old) {
+__device__ __forceinline__ void add16(float (&v)[N], u32x4_any old) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if constexpr (BF16) {
@@ -72,21 +65,21 @@ __device__ __forceinline__ void add16(float (&v)[N], u32x4 old) {
 }
 template <bool BF16, bool STREAM = true, int N>
 __device__ __forceinline__ void store16(void* out, long long at, const float (&v)[N]) {
-    u32x4 w;
+    u32x4_any w;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if constexpr (BF16) w[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
         else w[q] = __float_as_uint(v[q]);
     }
-    u32x4* const to = reinterpret_cast<u32x4*>(reinterpret_cast<char*>(out) + at * (BF16 ? 2 : 4));
+    u32x4_any* const to = reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(out) + at * (BF16 ? 2 : 4));
     if constexpr (STREAM) __builtin_nontemporal_store(w, to);
     else *to = w;                                           // a part that is read again at once
 }
 
 // Writes (or adds) up to N neighbours of a row of out, `left` of them inside it; N entries are 16 bytes.
 template <bool BF16, bool ADD, int N>
-__device__ __forceinline__ void put(void* out, long long at, float (&v)[N], int left, bool vec) {
-    if (vec && left >= N) {
+__device__ __forceinline__ void put(void* out, long long at, float (&v)[N], int left) {
+    if (left >= N) {
         if constexpr (ADD) add16<BF16>(v, load16<BF16>(out, at));
         store16<BF16>(out, at, v);
     } else {
@@ -104,14 +97,21 @@ __device__ __forceinline__ void put(void* out, long long at, float (&v)[N], int 
 
 // Writes (or adds) up to four neighbours of a row of out, `left` of them inside it.
 template <bool BF16>
-__device__ __forceinline__ void put4(void* out, long long at, f32x4 v, int left, bool vec, bool add) {
-    if (vec && left >= 4) {
-        if (add) {
-            const float4 o = load_grad4<BF16>(out, at / 4);
-            v += f32x4{o.x, o.y, o.z, o.w};
+__device__ __forceinline__ void put4(void* out, long long at, f32x4 v, int left, bool add) {
+    if (left >= 4) {
+        if constexpr (BF16) {
+            u32x2_any* to = reinterpret_cast<u32x2_any*>(reinterpret_cast<unsigned short*>(out) + at);
+            if (add) {
+                const u32x2_any o = *to;
+                v += f32x4{__uint_as_float(o[0] << 16), __uint_as_float(o[0] & 0xFFFF0000u), __uint_as_float(o[1] << 16),
+                           __uint_as_float(o[1] & 0xFFFF0000u)};
+            }
+            *to = u32x2_any{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        } else {
+            f32x4_any* to = reinterpret_cast<f32x4_any*>(reinterpret_cast<float*>(out) + at);
+            if (add) v += *to;
+            *to = v;
         }
-        if constexpr (BF16) reinterpret_cast<uint2*>(out)[at / 4] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        else reinterpret_cast<f32x4*>(out)[at / 4] = v;
     } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -227,7 +227,6 @@ __global__ __launch_bounds__(W * 64) void mxfp4_wave(const Operand A, const Oper
         }
     __syncthreads();
     const int used = min(W, units);
-    const bool vec = ldo % 4 == 0;
     for (int q = threadIdx.x; q < TM * TN / 4; q += W * 64) {
         const int r = q / (TN / 4), quad = q % (TN / 4), at = r * TN + ((quad ^ r) & (TN / 4 - 1)) * 4;
         f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][at]);
@@ -235,8 +234,8 @@ __global__ __launch_bounds__(W * 64) void mxfp4_wave(const Operand A, const Oper
         const int row = i0 + r, col = j0 + quad * 4;
         if (row >= A.rows || col >= B.rows) continue;
         const long long to = row * ldo + col;
-        if (bf16) put4<true>(out, to, v, B.rows - col, vec, add);
-        else put4<false>(out, to, v, B.rows - col, vec, add);
+        if (bf16) put4<true>(out, to, v, B.rows - col, add);
+        else put4<false>(out, to, v, B.rows - col, add);
     }
 }
 
@@ -503,10 +502,10 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
     static_assert(NW * 32 * COLS * 4 <= 2 * PAIR, "the results' regions must fit");
     float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * COLS;
     const int col = j0 + wn * COLS + (lane % PER_ROW) * WIDE, row0 = i0 + wm * (BM / WM) + lane / PER_ROW;
-    const bool vec = ldo % WIDE == 0, inside = vec && i0 + BM <= A.rows && j0 + BN <= B.rows;
+    const bool inside = i0 + BM <= A.rows && j0 + BN <= B.rows;
 #pragma unroll
     for (int x = 0; x < MI; ++x) {
-        u32x4 old[32 / AT_ONCE];
+        u32x4_any old[32 / AT_ONCE];
         if (ADD && inside) {
 #pragma unroll
             for (int t = 0; t < 32 / AT_ONCE; ++t) old[t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
@@ -535,7 +534,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
                 if constexpr (ADD) add16<BF16>(v, old[t]);
                 store16<BF16, OUT != OUT_PART>(out, row * ldo + col, v);
             } else if (row < A.rows) {
-                put<BF16, ADD, WIDE>(out, row * ldo + col, v, B.rows - col, vec);
+                put<BF16, ADD, WIDE>(out, row * ldo + col, v, B.rows - col);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -548,7 +547,6 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void mxfp4_join(const float* parts, int splits, long long split_floats, int m, int n, int ldp,
                                                   void* out, long long ldo, bool add) {
     const unsigned quads = ldp / 4;
-    const bool vec = ldo % 4 == 0;
     for (long long q = blockIdx.x * 256ll + threadIdx.x; q < static_cast<long long>(m) * quads; q += gridDim.x * 256ll) {
         const int row = static_cast<int>(q / quads), col = static_cast<int>(q % quads) * 4;
         f32x4 part[MAX_SPLITS];                              // loaded together, then added in order
@@ -559,7 +557,7 @@ __global__ __launch_bounds__(256) void mxfp4_join(const float* parts, int splits
 #pragma unroll
         for (int s = 1; s < MAX_SPLITS; ++s)
             if (s < splits) v += part[s];
-        put4<BF16>(out, row * ldo + col, v, n - col, vec, add);
+        put4<BF16>(out, row * ldo + col, v, n - col, add);
     }
 }
 

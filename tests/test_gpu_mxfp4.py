@@ -135,13 +135,20 @@ def extremes():
     return out
 
 
-def test_quantize_extremes():
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_extremes(dtype):
     gc = lib()
     x = extremes()
+    if dtype == "bf16":                                      # cut to bf16 bits, so that borders and subnormals stay among them
+        x = (x.view(np.uint32) >> 16).astype(np.uint16)
+        x[np.isnan(extremes())] = 0x7FC0
     for a in (x, np.ascontiguousarray(x.reshape(1, -1)), np.ascontiguousarray(x.T)):
-        print(f"case: mxfp4 quantize extremes {a.shape}", flush=True)
+        print(f"case: mxfp4 quantize extremes {a.shape} {dtype}", flush=True)
         r, c = Held(*a.shape), Held(*a.shape[::-1])
-        gc.gc_mxfp4_quantize(to_dev(a), *r.pair, *c.pair)
+        at = to_dev(np.ascontiguousarray(a).ravel()).view(*a.shape)
+        gc.gc_mxfp4_quantize(at, *r.pair)
+        same(r, oracle.mxfp4_quantize(a))
+        gc.gc_mxfp4_quantize(at, *r.pair, *c.pair)
         same(r, oracle.mxfp4_quantize(a))
         same(c, oracle.mxfp4_quantize(np.ascontiguousarray(a.T)))
 
