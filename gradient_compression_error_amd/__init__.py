@@ -489,72 +489,83 @@ def gc_mxfp4_scale_bytes(rows: int, cols: int) -> int:
 
 
 # Small calls are bound by the host, so these wrappers check in plain ifs (no
-# message is formed unless it is raised) and take the stream's handle directly.
+# message is formed unless it is raised), take a matrix's checks and addresses in
+# one helper, and take the stream's handle directly.
 _torch = None
+_u8 = None
+_codes_of = {}          # dtype -> GC_F32 / GC_BF16
 
 
-def _mx_torch():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
+def _mx_load():
+    """torch, loaded with the first call."""
+    global _torch, _u8
+    import torch
+    _u8 = torch.uint8
+    _codes_of.update({torch.float32: GC_F32, torch.bfloat16: GC_BF16})
+    _torch = torch
 
 
-def _mx_held(torch, codes, scales, rows: int, cols: int, name: str):
-    """An MXFP4 matrix's two buffers: uint8, with room for the shape."""
-    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+def _mx_dtype(t, name: str) -> int:
+    code = _codes_of.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype} not supported (float32 or bfloat16)")
+    return code
+
+
+def _mx_elsewhere(t):
+    raise ValueError("expected a device tensor" if t.get_device() < 0 else "every tensor must be on the same device")
+
+
+def _mx_held(codes, scales, rows: int, cols: int, dev: int, name: str):
+    """Addresses of an MXFP4 matrix's two buffers: uint8, contiguous, with room for the shape, on device dev."""
+    if codes.dtype is not _u8 or scales.dtype is not _u8:
         raise TypeError(f"{name} codes and scales: expected torch.uint8, got {codes.dtype} and {scales.dtype}")
     units = rows * ((cols + 127) >> 7)
     if codes.numel() < 64 * units:
         raise ValueError(f"{name} codes need gc_mxfp4_code_bytes entries")
     if scales.numel() < 4 * units:
         raise ValueError(f"{name} scales need gc_mxfp4_scale_bytes entries")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    if codes.get_device() != dev:
+        _mx_elsewhere(codes)
+    if scales.get_device() != dev:
+        _mx_elsewhere(scales)
+    return codes.data_ptr(), scales.data_ptr()
 
 
 def _mx_pitched(t, name: str):
     """(rows, cols, entries between rows) of a matrix whose rows are contiguous (a vector is one row)."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 1:
-        rows, cols, ld = 1, shape[0], shape[0]
-    elif len(shape) == 2:
+    shape = t.shape
+    if len(shape) == 2:
         rows, cols = shape
-        ld = cols if rows == 1 else stride[0]
+        ld, step = t.stride()
+        if rows == 1:
+            ld = cols
+    elif len(shape) == 1:
+        rows, cols = 1, shape[0]
+        ld, step = cols, t.stride(0)
     else:
-        rows = cols = ld = 0
+        rows = cols = 0
     if rows < 1 or cols < 1:
         raise ValueError(f"{name} must be a vector or a matrix with entries")
-    if cols > 1 and stride[-1] != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
     if ld < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
     return rows, cols, ld
 
 
-def _mx_device(t) -> int:
-    dev = t.get_device()
+def _mx_call(dev: int, stream, where: str, fn, args) -> None:
+    """fn(*args, stream) with device dev current, on the given stream or that device's current one."""
     if dev < 0:
         raise ValueError("expected a device tensor")
-    return dev
-
-
-def _mx_ptr(t, dev: int, contiguous: bool = True):
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise ValueError("expected a device tensor" if t.get_device() < 0 else "every tensor must be on the same device")
-    if contiguous and not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _mx_call(torch, dev: int, stream, where: str, fn, *args) -> None:
-    """fn(*args, stream) with device dev current, on the given stream or that device's current one."""
+    torch = _torch
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -565,65 +576,80 @@ def _mx_call(torch, dev: int, stream, where: str, fn, *args) -> None:
 
 def gc_mxfp4_ef_encode(grad, mem, eta: float, codes, scales, stream=None) -> None:
     """MXFP4 step with memory: (codes, scales) <- Q(mem + eta*grad), mem <- what the message leaves out."""
-    torch = _mx_torch()
-    if mem.dtype is not torch.float32:
+    if _torch is None:
+        _mx_load()
+    if mem.dtype is not _torch.float32:
         raise TypeError(f"mem: expected torch.float32, got {mem.dtype}")
-    d = mem.numel()
+    d, dev = mem.numel(), mem.get_device()
     if d < 1 or grad.numel() != d:
         raise ValueError("grad and mem must have the same number of entries, at least one")
-    _mx_held(torch, codes, scales, 1, d, "message")
-    dev = _mx_device(mem)
-    _mx_call(torch, dev, stream, "gc_mxfp4_ef_encode", lib.gc_mxfp4_ef_encode, _mx_ptr(grad, dev), _dtype_code(grad),
-             _mx_ptr(mem, dev), d, float(eta), _mx_ptr(codes, dev), _mx_ptr(scales, dev))
+    if not grad.is_contiguous() or not mem.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    pc, ps = _mx_held(codes, scales, 1, d, dev, "message")
+    if grad.get_device() != dev:
+        _mx_elsewhere(grad)
+    _mx_call(dev, stream, "gc_mxfp4_ef_encode", lib.gc_mxfp4_ef_encode,
+             (grad.data_ptr(), _mx_dtype(grad, "grad"), mem.data_ptr(), d, float(eta), pc, ps))
 
 
 def gc_mxfp4_decode(codes, scales, out, weight: float = 1.0, accumulate: bool = False, stream=None) -> None:
     """out = [out +] weight * the sum of the messages' values.  out: a vector, or
     a matrix (dense).  codes and scales: one message (1-D), or one a row (2-D, as
     an all-gather leaves them; the rows may be further apart than their length)."""
-    torch = _mx_torch()
-    shape = out.shape
+    if _torch is None:
+        _mx_load()
+    shape, dev = out.shape, out.get_device()
     if len(shape) not in (1, 2) or out.numel() < 1:
         raise ValueError("out must be a vector or a matrix with entries")
+    if not out.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
     rows, cols = (1, shape[0]) if len(shape) == 1 else shape
-    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
-        raise TypeError(f"codes and scales: expected torch.uint8, got {codes.dtype} and {scales.dtype}")
-    nc, ns = codes.shape, scales.shape
-    if len(nc) != len(ns) or len(nc) not in (1, 2):
-        raise ValueError("codes and scales must both be 1-D or 2-D")
-    nmsg = 1 if len(nc) == 1 else nc[0]
-    if nmsg < 1 or (len(ns) == 2 and ns[0] != nmsg):
-        raise ValueError("codes and scales need one row per message")
-    units = rows * ((cols + 127) >> 7)
-    if nc[-1] < 64 * units:
-        raise ValueError("codes need gc_mxfp4_code_bytes entries a message")
-    if ns[-1] < 4 * units:
-        raise ValueError("scales need gc_mxfp4_scale_bytes entries a message")
-    if codes.stride(-1) != 1 or scales.stride(-1) != 1:
-        raise ValueError("a message must be contiguous")
-    cs, ss = (codes.stride(0), scales.stride(0)) if nmsg > 1 else (0, 0)
-    dev = _mx_device(out)
-    _mx_call(torch, dev, stream, "gc_mxfp4_decode", lib.gc_mxfp4_decode, _mx_ptr(codes, dev, False),
-             _mx_ptr(scales, dev, False), nmsg, cs, ss, rows, cols, float(weight), _mx_ptr(out, dev), _dtype_code(out),
-             1 if accumulate else 0)
+    nmsg, cs, ss = 1, 0, 0
+    if len(codes.shape) == 1 and len(scales.shape) == 1:
+        pc, ps = _mx_held(codes, scales, rows, cols, dev, "message")
+    else:
+        if codes.dtype is not _u8 or scales.dtype is not _u8:
+            raise TypeError(f"codes and scales: expected torch.uint8, got {codes.dtype} and {scales.dtype}")
+        if len(codes.shape) != 2 or len(scales.shape) != 2:
+            raise ValueError("codes and scales must both be 1-D or 2-D")
+        nmsg = codes.shape[0]
+        if nmsg < 1 or scales.shape[0] != nmsg:
+            raise ValueError("codes and scales need one row per message")
+        units = rows * ((cols + 127) >> 7)
+        if codes.shape[1] < 64 * units:
+            raise ValueError("codes need gc_mxfp4_code_bytes entries a message")
+        if scales.shape[1] < 4 * units:
+            raise ValueError("scales need gc_mxfp4_scale_bytes entries a message")
+        (cs, c1), (ss, s1) = codes.stride(), scales.stride()
+        if c1 != 1 or s1 != 1:
+            raise ValueError("a message must be contiguous")
+        if codes.get_device() != dev:
+            _mx_elsewhere(codes)
+        if scales.get_device() != dev:
+            _mx_elsewhere(scales)
+        pc, ps = codes.data_ptr(), scales.data_ptr()
+    _mx_call(dev, stream, "gc_mxfp4_decode", lib.gc_mxfp4_decode,
+             (pc, ps, nmsg, cs, ss, rows, cols, float(weight), out.data_ptr(), _mx_dtype(out, "out"), 1 if accumulate else 0))
 
 
 def gc_mxfp4_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, stream=None) -> None:
     """Q of a matrix along its rows (codes, scales: rows x cols), along its columns
     (codes_t, scales_t: cols x rows, transposed), or both.  x may be a view with a row pitch."""
-    torch = _mx_torch()
+    if _torch is None:
+        _mx_load()
     rows, cols, ld = _mx_pitched(x, "x")
     if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
         raise ValueError("a form needs codes and scales")
-    if codes is None and codes_t is None:
-        raise ValueError("no output given")
+    dev = x.get_device()
+    pc = ps = pct = pst = None
     if codes is not None:
-        _mx_held(torch, codes, scales, rows, cols, "row")
+        pc, ps = _mx_held(codes, scales, rows, cols, dev, "row")
     if codes_t is not None:
-        _mx_held(torch, codes_t, scales_t, cols, rows, "column")
-    dev = _mx_device(x)
-    _mx_call(torch, dev, stream, "gc_mxfp4_quantize", lib.gc_mxfp4_quantize, x.data_ptr(), _dtype_code(x), rows, cols, ld,
-             _mx_ptr(codes, dev), _mx_ptr(scales, dev), _mx_ptr(codes_t, dev), _mx_ptr(scales_t, dev))
+        pct, pst = _mx_held(codes_t, scales_t, cols, rows, dev, "column")
+    if pc is None and pct is None:
+        raise ValueError("no output given")
+    _mx_call(dev, stream, "gc_mxfp4_quantize", lib.gc_mxfp4_quantize,
+             (x.data_ptr(), _mx_dtype(x, "x"), rows, cols, ld, pc, ps, pct, pst))
 
 
 def gc_mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -633,17 +659,24 @@ def gc_mxfp4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
 def gc_mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, k: int, out, ws=None, accumulate: bool = False,
                     stream=None) -> None:
     """out [m, n] = [out +] A B^T for MXFP4 matrices A (m x k) and B (n x k); out may be a view with a row pitch."""
-    torch = _mx_torch()
+    if _torch is None:
+        _mx_load()
     m, n, ldo = _mx_pitched(out, "out")
     k = int(k)
     if k < 1:
         raise ValueError("k must be at least 1")
-    _mx_held(torch, a_codes, a_scales, m, k, "A")
-    _mx_held(torch, b_codes, b_scales, n, k, "B")
-    dev = _mx_device(out)
-    _mx_call(torch, dev, stream, "gc_mxfp4_matmul", lib.gc_mxfp4_matmul, _mx_ptr(a_codes, dev), _mx_ptr(a_scales, dev),
-             _mx_ptr(b_codes, dev), _mx_ptr(b_scales, dev), m, n, k, out.data_ptr(), ldo, _dtype_code(out),
-             1 if accumulate else 0, _mx_ptr(ws, dev), 0 if ws is None else ws.nbytes)
+    dev = out.get_device()
+    pac, pas = _mx_held(a_codes, a_scales, m, k, dev, "A")
+    pbc, pbs = _mx_held(b_codes, b_scales, n, k, dev, "B")
+    pw, wb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev:
+            _mx_elsewhere(ws)
+        if not ws.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        pw, wb = ws.data_ptr(), ws.nbytes
+    _mx_call(dev, stream, "gc_mxfp4_matmul", lib.gc_mxfp4_matmul,
+             (pac, pas, pbc, pbs, m, n, k, out.data_ptr(), ldo, _mx_dtype(out, "out"), 1 if accumulate else 0, pw, wb))
 
 
 # ------------------------------------------------------------------ timing hooks
