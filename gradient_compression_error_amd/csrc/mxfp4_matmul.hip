@@ -260,6 +260,13 @@ __device__ __forceinline__ void wait_for() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(VM) : "memory");
 }
 
+// All waves of the workgroup; no memory access is moved over it by the compiler.
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // Waits until at most N of this wave's LDS reads are outstanding.
 template <int N>
 __device__ __forceinline__ void wait_reads() {
@@ -311,6 +318,26 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
     // this workgroup's part of k: per_split groups (a multiple of 4) from `begin` on
     const int begin = split * per_split, groups = min(per_split, row_groups - begin);
 
+    // With registers to spare (EARLY) both operands' fragments are held twice, so a
+    // stage's reads are issued a whole stage ahead; else only B's, the smaller, are.
+    constexpr bool EARLY = MI * NI <= 4;
+
+    // A lane's part of out, 16 bytes of PER_ROW lanes a row.  What is added to is
+    // fetched here, under the work, where a workgroup has a compute unit to itself and
+    // registers for it (4096 x 1024 x 8192 added to float32: 29.4 us, 30.8 fetched at the end).
+    constexpr bool AHEAD = ADD && EARLY && R == 4;
+    constexpr int COLS = NI * 32, WIDE = BF16 ? 8 : 4, PER_ROW = COLS / WIDE, AT_ONCE = 64 / PER_ROW;
+    const int wm = wave / WN, wn = wave % WN;
+    const int col = j0 + wn * COLS + (lane % PER_ROW) * WIDE, row0 = i0 + wm * (BM / WM) + lane / PER_ROW;
+    const bool inside = i0 + BM <= A.rows && j0 + BN <= B.rows;
+    u32x4_any old[AHEAD ? MI : 1][32 / AT_ONCE];
+    if (AHEAD && inside) {
+#pragma unroll
+        for (int x = 0; x < MI; ++x)
+#pragma unroll
+            for (int t = 0; t < 32 / AT_ONCE; ++t) old[x][t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
+    }
+
     // Where this wave's copies come from: a uniform base per operand and a lane's
     // offset (below 2^32: a tile's rows are at most 256 times 2^23 bytes).  Rows
     // past the operand are its last row again; their results are not written.
@@ -354,7 +381,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
     };
 
     // Where this wave's fragments lie.
-    const int wm = wave / WN, wn = wave % WN, half = lane >> 5, i = lane & 31;
+    const int half = lane >> 5, i = lane & 31;
     const int a_at = wm * MI * 4096 + i * 128, b_at = BM * 128 + wn * NI * 4096 + i * 128;
     const int as_at = wm * MI * 512 + i * 16 + 2 * half, bs_at = BM * 16 + wn * NI * 512 + i * 16 + 2 * half;
     int c_at[2][2];                                          // byte of a row, by group of the pair and u
@@ -401,10 +428,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
         for (int c = 0; c < CP; ++c) copy_code(c, p, p);
     }
     wait_for<(D - 1) * SP + (R - 1) * CP>();
-    __builtin_amdgcn_s_barrier();
-    // With registers to spare (EARLY) both operands' fragments are held twice, so a
-    // stage's reads are issued a whole stage ahead; else only B's, the smaller, are.
-    constexpr bool EARLY = MI * NI <= 4;
+    meet();
     i32x4 fa0[MI][2], fa1[EARLY ? MI : 1][2], fb0[NI][2], fb1[NI][2];
     int sa0[MI], sa1[EARLY ? MI : 1], sb0[NI], sb1[NI];
 #pragma unroll
@@ -425,7 +449,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
         if constexpr (G == 1) {
             wait_for<(R - 2) * (CP + SP / 2)>();            // the next pair has landed
             if constexpr (EARLY) wait_reads<0>();           // (issued a stage ago) and nobody reads this one any more
-            __builtin_amdgcn_s_barrier();
+            meet();
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (EARLY) {
@@ -454,7 +478,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
                     // here nobody reads this pair any more
                     __builtin_amdgcn_sched_barrier(0);
                     wait_reads<6>();
-                    __builtin_amdgcn_s_barrier();
+                    meet();
                 } else {
                     constexpr int FROM = EARLY ? 0 : 1;
 #pragma unroll
@@ -492,23 +516,19 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
     if (rest > 1) odd(k0, k1);
     if (rest > 2) even(k1, k0);
     wait_for<0>();
-    __builtin_amdgcn_s_barrier();                            // every copy has landed, every fragment is read: LDS is free
+    meet();                                                  // every copy has landed, every fragment is read: LDS is free
 
     out = static_cast<char*>(out) + split * split_stride;
 
     // Results go through LDS, a row of fragments at a time in a region of the
     // wave's own, so that memory sees whole rows of the wave's columns.
-    constexpr int COLS = NI * 32, WIDE = BF16 ? 8 : 4, PER_ROW = COLS / WIDE, AT_ONCE = 64 / PER_ROW;
     static_assert(NW * 32 * COLS * 4 <= 2 * PAIR, "the results' regions must fit");
     float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * COLS;
-    const int col = j0 + wn * COLS + (lane % PER_ROW) * WIDE, row0 = i0 + wm * (BM / WM) + lane / PER_ROW;
-    const bool inside = i0 + BM <= A.rows && j0 + BN <= B.rows;
 #pragma unroll
     for (int x = 0; x < MI; ++x) {
-        u32x4_any old[32 / AT_ONCE];
-        if (ADD && inside) {
+        if (ADD && !AHEAD && inside) {
 #pragma unroll
-            for (int t = 0; t < 32 / AT_ONCE; ++t) old[t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
+            for (int t = 0; t < 32 / AT_ONCE; ++t) old[0][t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
         }
 #pragma unroll
         for (int y = 0; y < NI; ++y)
@@ -531,7 +551,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
                 v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
             }
             if (inside) {
-                if constexpr (ADD) add16<BF16>(v, old[t]);
+                if constexpr (ADD) add16<BF16>(v, old[AHEAD ? x : 0][t]);
                 store16<BF16, OUT != OUT_PART>(out, row * ldo + col, v);
             } else if (row < A.rows) {
                 put<BF16, ADD, WIDE>(out, row * ldo + col, v, B.rows - col);

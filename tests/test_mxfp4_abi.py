@@ -77,7 +77,7 @@ def test_matmul_refusals(gcl):  # noqa: F811
 
     for kw in [dict(ac=None), dict(as_=None), dict(bc=None), dict(bs=None), dict(out=None), dict(ac=AC + 8),
                dict(bs=BS + 4), dict(out=X + 8), dict(m=0), dict(n=0), dict(k=0), dict(m=2**31), dict(n=2**31),
-               dict(k=2**31), dict(m=2**26, k=2**20), dict(m=2**20, n=2**20), dict(ldo=49), dict(ldo=2**35),
+               dict(k=2**31), dict(k=2**24 + 1), dict(m=2**26, k=2**20), dict(m=2**20, n=2**20), dict(ldo=49), dict(ldo=2**35),
                dict(out=AC + 64), dict(out=AS), dict(out=BC + 64), dict(out=BS - 16)]:
         assert call(**kw) == gcl.GC_ERR_ARG, kw
     assert call(dt=4) == gcl.GC_ERR_DTYPE
