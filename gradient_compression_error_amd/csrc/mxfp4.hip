@@ -5,12 +5,12 @@
 //     s = max(E(max |x|) - 2, 0)      E: biased float32 exponent
 //     code = RNE_E2M1(x * 2^(127 - s)), saturating at 6
 // so the largest entry lands in [4, 8) and the step is 2^(s - 127) times 0.5,
-// 1 or 2 by binade.  x * 2^(127 - s) is exact where it matters: it can only
-// lose bits below 2^-126, far under the first rounding border at 0.25.
-// A block with an entry that is not finite gets s = 255 (NaN) and zero codes.
+// 1 or 2 by binade.  The conversion instructions take the scale as an operand and
+// round once.  A block with an entry that is not finite gets s = 255 (NaN) and zero
+// codes.
 //
-// All kernels here are bound by HBM traffic: about 10 operations per entry
-// against 2.5 to 12.5 bytes.
+// Encode, decode and quantisation along one axis are bound by HBM traffic (2.5 to
+// 12.5 bytes an entry), small calls by the launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -249,7 +249,8 @@ __global__ __launch_bounds__(MX_THREADS) void mxfp4_ef(const void* grad, float* 
     }
 }
 
-// Quantisation along the rows.  A thread takes eight columns, four lanes a block.
+// Quantisation along the rows.  A thread takes eight columns, four lanes a block, so
+// that a wave reads 1 KiB of bf16 together.  8192 x 4096 bf16: 14.2 us, 6.0 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(MX_THREADS) void mxfp4_rows(const void* x, long long ld, long long units, unsigned per_row,
                                                          long long cols, unsigned* codes, unsigned* scales) {
@@ -279,7 +280,9 @@ __global__ __launch_bounds__(MX_THREADS) void mxfp4_rows(const void* x, long lon
 // column block lanes 16 apart, and a lane's eight codes of a column one word of its 16
 // bytes.  The words meet in LDS, at places that keep the banks apart, and leave 16
 // bytes a lane, 64 of a row or column together: stored word by word they took 11 of 29
-// us (8192 x 4096 bf16, both forms).  Tiles go down four and along on an XCD, since
+// us (8192 x 4096 bf16, both forms).  Both take 25.7 us now, 4.0 TB/s (a kernel for
+// each: 58), the columns alone 14.6: what the second form adds is its conversions and
+// its way through LDS.  Tiles go down four and along on an XCD, since
 // neighbours share lines of either form's codes and scales.
 template <bool BF16, bool ROWS>
 __global__ __launch_bounds__(MX_THREADS) void mxfp4_cols(const void* x, long long ld, long long rows, long long cols,
@@ -406,8 +409,9 @@ __global__ __launch_bounds__(MX_THREADS) void mxfp4_cols(const void* x, long lon
 }
 
 // out = [out +] weight * sum over the messages of their values, added in message
-// order in float32 and rounded once to the output type.  A thread writes 16 bytes; four
-// messages' codes are in flight at a time.
+// order in float32 and rounded once to the output type.  A thread writes 16 bytes (32
+// to float32 from several messages); four messages' codes are in flight at a time.
+// 25.6M float32 entries of one message: 17.6 us, 6.6 TB/s.
 template <bool BF16, bool ADD, bool FLAT, int N>
 __global__ __launch_bounds__(MX_THREADS) void mxfp4_decode(const unsigned char* codes, const unsigned char* scales,
                                                            int nmsg, long long code_stride, long long scale_stride,
