@@ -632,9 +632,12 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
         best.per_split = ((groups + splits - 1) / splits + 3) / 4 * 4;
         best.splits = (groups + best.per_split - 1) / best.per_split;
     };
-    // several of these fit a compute unit, the last two alone: whole rounds
+    // several of these fit a compute unit, the last two alone: whole rounds.  A launch
+    // holds fewer than 2^32 threads, 512 a workgroup.
     auto wave = [&](Plan::Kind kind, int mi, int ni, double per_group, bool whole) {
-        const double r = std::max(1.0, tiles_of(m, n, 16 * mi, 16 * ni) / 256.0);
+        const int64_t tiles = tiles_of(m, n, 16 * mi, 16 * ni);
+        if (tiles > int64_t(1) << 22) return;
+        const double r = std::max(1.0, tiles / 256.0);
         offer(kind, 2.5 + per_group * g * (whole ? std::ceil(r) : r), 1);
     };
     wave(Plan::WAVE_1_1, 1, 1, 0.08, false);

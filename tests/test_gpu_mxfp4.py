@@ -606,6 +606,27 @@ def test_ef_past_32_bits():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("turned", [False, True])
+def test_product_of_a_vector_and_2_27_rows(turned):
+    """The most rows of an operand against one: 2^23 tiles of 16 x 16 would be 2^32 threads of one launch."""
+    gc = lib()
+    rows, k = 1 << 27, 32
+    print(f"case: mxfp4 matmul {1 if turned else rows}x{rows if turned else 1}x{k}", flush=True)
+    r = gen.rng(0, gen.KIND_MISC, 507)
+    a, part = random_held(r, 1, k, 126, 127), random_held(r, 4096, k, 126, 127)
+    bc = torch.from_numpy(part[0].reshape(4096, 64)).to(DEV).repeat(rows // 4096, 1)
+    bs = torch.from_numpy(part[1].reshape(4096, 4)).to(DEV).repeat(rows // 4096, 1)
+    out = torch.empty((1, rows) if turned else (rows, 1), device=DEV)
+    m, n = out.shape
+    ws = torch.empty(max(16, gc.gc_mxfp4_matmul_workspace_bytes(m, n, k)), dtype=torch.uint8, device=DEV)
+    one, many = held_from(*a), (bc.view(-1), bs.view(-1))
+    gc.gc_mxfp4_matmul(*(one + many if turned else many + one), k, out, ws)
+    want = torch.from_numpy(oracle.mxfp4_matmul(part, a, k).astype(np.float32)).to(DEV).view(-1)
+    assert torch.equal(out.view(-1, 4096), want[None].expand(rows // 4096, 4096))
+    del bc, bs, many, out
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("m", [1, 40])
 def test_product_past_32_bits(m):
     """An operand of more than 2^32 bytes of codes: rows at its start, across the border and at its end."""
