@@ -18,6 +18,9 @@ inline bool mx_shape_ok(int64_t rows, int64_t cols) {
 constexpr int64_t MX_MAX_DIM = int64_t(1) << 30;       // rows or columns of a product
 constexpr int64_t MX_MAX_K = int64_t(1) << 24;         // its depth: 256 rows of codes stay within 32-bit offsets
 
+constexpr int MX_MAX_MESSAGES = 1 << 20;               // of a decode; with strides of up to 2^40 bytes
+constexpr int64_t MX_MAX_SPAN = int64_t(1) << 40;      // entries between a pitched matrix's first and last row
+
 int mx_check_matrix(const char* fn, const char* name, const void* codes, const void* scales);
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -585,7 +585,7 @@ int gc_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int nmsg, int64
     if (out_dtype != GC_F32 && out_dtype != GC_BF16)
         return fail(GC_ERR_DTYPE, "gc_mxfp4_decode: out_dtype must be GC_F32 or GC_BF16");
     if (!mx_shape_ok(rows, cols)) return fail(GC_ERR_ARG, "gc_mxfp4_decode: rows or cols out of range");
-    if (nmsg < 1) return fail(GC_ERR_ARG, "gc_mxfp4_decode: nmsg must be at least 1");
+    if (nmsg < 1 || nmsg > MX_MAX_MESSAGES) return fail(GC_ERR_ARG, "gc_mxfp4_decode: nmsg must be in [1, 2^20]");
     const int64_t cb = mx_code_bytes(rows, cols), sb = mx_scale_bytes(rows, cols);
     if (nmsg > 1) {
         if (code_stride < cb || code_stride % 16 != 0 || code_stride > (int64_t(1) << 40))
@@ -619,6 +619,7 @@ int gc_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int6
     if (!mx_shape_ok(rows, cols) || (by_cols && !mx_shape_ok(cols, rows)))
         return fail(GC_ERR_ARG, "gc_mxfp4_quantize: rows or cols out of range");
     if (ld < cols || ld > MX_MAX_ENTRIES) return fail(GC_ERR_ARG, "gc_mxfp4_quantize: ld must be in [cols, 2^34]");
+    if (rows - 1 > MX_MAX_SPAN / ld) return fail(GC_ERR_ARG, "gc_mxfp4_quantize: (rows - 1) * ld must be at most 2^40");
     int rc;
     if (by_rows && (rc = mx_check_matrix(fn, "row", codes, scales)) != GC_OK) return rc;
     if (by_cols && (rc = mx_check_matrix(fn, "column", codes_t, scales_t)) != GC_OK) return rc;

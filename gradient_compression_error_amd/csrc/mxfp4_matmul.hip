@@ -711,6 +711,7 @@ int gc_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8
     if (!matmul_shape_ok(m, n, k))
         return fail(GC_ERR_ARG, "gc_mxfp4_matmul: m, n or k out of range");
     if (ldo < n || ldo > MX_MAX_ENTRIES) return fail(GC_ERR_ARG, "gc_mxfp4_matmul: ldo must be in [n, 2^34]");
+    if (m - 1 > MX_MAX_SPAN / ldo) return fail(GC_ERR_ARG, "gc_mxfp4_matmul: (m - 1) * ldo must be at most 2^40");
     const size_t ob = static_cast<size_t>((m - 1) * ldo + n) * (out_dtype == GC_BF16 ? 2 : 4);
     if (overlaps(out, ob, a_codes, mx_code_bytes(m, k)) || overlaps(out, ob, a_scales, mx_scale_bytes(m, k)) ||
         overlaps(out, ob, b_codes, mx_code_bytes(n, k)) || overlaps(out, ob, b_scales, mx_scale_bytes(n, k)))

@@ -361,7 +361,7 @@ size_t gc_mxfp4_scale_bytes(int64_t rows, int64_t cols);
 int gc_mxfp4_ef_encode(const void* grad, int grad_dtype, float* mem, int64_t d, float eta, uint8_t* codes,
                        uint8_t* scales, void* stream);
 
-/* Decode of nmsg >= 1 messages of the same shape, as an all-gather leaves them:
+/* Decode of nmsg messages (1 to 2^20) of the same shape, as an all-gather leaves them:
  *     out = [out +] fl32(weight * sum_i D(message i))
  * The sum is taken in float32 in message order; out [rows x cols], dense, is
  * float32 or bf16 (out_dtype; one rounding at the end).  accumulate != 0 adds
@@ -373,8 +373,8 @@ int gc_mxfp4_ef_encode(const void* grad, int grad_dtype, float* mem, int64_t d, 
 int gc_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int nmsg, int64_t code_stride, int64_t scale_stride,
                     int64_t rows, int64_t cols, float weight, void* out, int out_dtype, int accumulate, void* stream);
 
-/* Quantisation of a matrix x [rows x cols], rows ld entries apart (ld >= cols),
- * float32 or bf16, without memory: the operands of gc_mxfp4_matmul.
+/* Quantisation of a matrix x [rows x cols], rows ld entries apart (ld >= cols,
+ * (rows - 1) ld <= 2^40), float32 or bf16, without memory: the operands of gc_mxfp4_matmul.
  *   codes, scales      Q along the rows: the MXFP4 matrix rows x cols, or both NULL
  *   codes_t, scales_t  Q along the columns, transposed: the MXFP4 matrix
  *                      cols x rows, or both NULL
@@ -392,7 +392,7 @@ size_t gc_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 /* Product of two MXFP4 matrices, both with the summed index along their rows:
  *     out[i, j] = [out[i, j] +] sum_k D(A)[i, k] * D(B)[j, k]
  * A is m x k, B is n x k; out has m rows of n entries, ldo entries apart
- * (ldo >= n), float32 or bf16 (out_dtype).  Products are summed in float32 in
+ * (ldo >= n, (m - 1) ldo <= 2^40), float32 or bf16 (out_dtype).  Products are summed in float32 in
  * an order fixed by the sizes; out is rounded once.  Entries of out between
  * the rows (n .. ldo) are left alone.
  *   m, n     in [1, 2^30], k in [1, 2^24]; each matrix, and m x n, within the

@@ -53,6 +53,20 @@ def test_decode_refusals(gcl):  # noqa: F811
 
 
 @no_gpu
+def test_extents_past_64_bits_are_refused(gcl):  # noqa: F811
+    """Sizes whose last byte has no 64-bit offset: messages, rows of x and rows of out far apart."""
+    lib_ = gcl.lib
+    args = (2**40, 2**40, 1, 32, 1.0, X, 0, 0, None)
+    for nmsg in (2**31 - 1, 2**20 + 1):
+        assert lib_.gc_mxfp4_decode(C, S, nmsg, *args) == gcl.GC_ERR_ARG and "2^20" in gcl.gc_last_error(), nmsg
+    for rows in (2**27, 66):
+        assert lib_.gc_mxfp4_quantize(X, 0, rows, 32, 2**34, C, S, None, None, None) == gcl.GC_ERR_ARG
+        assert "2^40" in gcl.gc_last_error(), rows
+        assert lib_.gc_mxfp4_matmul(C, S, C, S, rows, 32, 32, X, 2**34, 0, 0, None, 0, None) == gcl.GC_ERR_ARG
+        assert "2^40" in gcl.gc_last_error(), rows
+
+
+@no_gpu
 def test_quantize_refusals(gcl):  # noqa: F811
     T, U = 0x6000000, 0x7000000
 
