@@ -9,7 +9,7 @@
 // What bounds it: for large products the chip's power (8192^3 with random codes:
 // 260 us, 4.2 PFLOP/s; 211 without the copies from memory, 158 with codes of zero); for
 // about one 128 x 128 tile a compute unit the copies into LDS and the matrix
-// instructions, which overlap in part (4096 x 1024 x 8192: 24.9 us, either alone about
+// instructions, which overlap in part (4096 x 1024 x 8192: 23.8 us, either alone about
 // 15); for few rows the read of B (16 x 8192 x 8192: 10.0 us, 3.6 TB/s); for small
 // calls the launch (1 x 4096 x 1024: 2.6 us).
 #include <algorithm>
@@ -291,7 +291,8 @@ __device__ __forceinline__ void wait_reads() {
 //   256 x 256, four waves of 128 x 128, R = 2: every operand byte read from LDS serves
 //       128 rows, and a lane holds 256 accumulators; with eight waves 290 against 278 us.
 //   128 x 128, eight waves of 64 x 32, R = 4: a compute unit for each of up to 256 tiles.
-//       4096 x 1024 x 8192: 24.6 us, 30.9 with the next, 48.8 with the first.
+//       4096 x 1024 x 8192: 23.8 us, 30.9 with the next, 48.8 with the first; 25.5 with
+//       two teams of four 64 x 64 waves that share k, which read a third less from LDS.
 //   128 x 128, four waves of 64 x 64, R = 2: two tiles a compute unit for more than 256.
 //       4096 x 2048 x 8192: 43.8 us, 51.8 with the one before, 53.0 with the first.
 //
@@ -336,10 +337,13 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
     // With registers to spare (EARLY) both operands' fragments are held twice, so a
     // stage's reads are issued a whole stage ahead; else only B's, the smaller, are.
     constexpr bool EARLY = MI * NI <= 4;
+    // With pairs to spare the second half of a pair's codes is copied a stage later,
+    // so that the copies are spread over all of the work (24.6 us -> 23.8).
+    constexpr int LATER = EARLY && R > 2 ? CP / 2 : 0, NOW = CP - LATER;
 
     // A lane's part of out, 16 bytes of PER_ROW lanes a row.  What is added to is
     // fetched here, under the work, where a workgroup has a compute unit to itself and
-    // registers for it (4096 x 1024 x 8192 added to float32: 29.4 us, 30.8 fetched at the end).
+    // registers for it (4096 x 1024 x 8192 added to float32: 29.4 us, 30.8 fetched at the end; 28.0 now).
     constexpr bool AHEAD = ADD && EARLY && R == 4;
     constexpr int COLS = NI * 32, WIDE = BF16 ? 8 : 4, PER_ROW = COLS / WIDE, AT_ONCE = 64 / PER_ROW;
     const int wm = wave / WN, wn = wave % WN;
@@ -428,8 +432,8 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[x][y][r] = 0.0f;
 
-    // Pairs 0 .. R - 1 and chunks 0 .. D - 1, from pair 2 on in the order of the loop,
-    // so that its wait counts hold from the start.
+    // Pairs 0 .. R - 1 (without what the loop's first stage copies) and chunks 0 .. D - 1,
+    // from pair 2 on in the order of the loop, so that its wait counts hold from the start.
 #pragma unroll
     for (int p = 0; p < R; ++p) {
         if (p < 2) {
@@ -440,9 +444,9 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
             for (int c = 0; c < SP / 2; ++c) copy_scale((p & 1) * (SP / 2) + c, 2 + (p - 2) / 2, 2 + (p - 2) / 2);
         }
 #pragma unroll
-        for (int c = 0; c < CP; ++c) copy_code(c, p, p);
+        for (int c = 0; c < (p == R - 1 ? NOW : CP); ++c) copy_code(c, p, p);
     }
-    wait_for<(D - 1) * SP + (R - 1) * CP>();
+    wait_for<(D - 1) * SP + (R - 1) * CP - LATER>();
     meet();
     i32x4 fa0[MI][2], fa1[EARLY ? MI : 1][2], fb0[NI][2], fb1[NI][2];
     int sa0[MI], sa1[EARLY ? MI : 1], sb0[NI], sb1[NI];
@@ -452,7 +456,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
     for (int x = 0; x < MI; ++x) read_a(fa0, sa0, x, {0, 0, 0, 0});
 
     // One stage, the first or second (G) of a pair, the first or second (P) of a
-    // chunk.  Pair p + R is copied during the second stage of pair p, into p's place,
+    // chunk.  Pair p + R is copied from the second stage of pair p on, into p's place,
     // and has landed when its first fragments are read, in the second stage of pair
     // p + R - 1.  Chunk c + D comes with the two pairs of chunk c, where chunk c - 1 was.
     int chunk = 0, ring = 0, pair = 0;                       // chunk, and the places of chunk and pair
@@ -498,13 +502,18 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
                 } else {
                     constexpr int FROM = EARLY ? 0 : 1;
 #pragma unroll
-                    for (int c = (x - FROM) * CP / (MI - FROM); c < (x - FROM + 1) * CP / (MI - FROM); ++c)
+                    for (int c = (x - FROM) * NOW / (MI - FROM); c < (x - FROM + 1) * NOW / (MI - FROM); ++c)
                         copy_code(c, 2 * chunk + P + R, pair);
                     if (x == MI - 1) {
 #pragma unroll
                         for (int c = 0; c < SP / 2; ++c) copy_scale(P * (SP / 2) + c, chunk + D, ring == 0 ? D : ring - 1);
                     }
                 }
+            }
+            if constexpr (G == 0 && LATER > 0) {
+#pragma unroll
+                for (int c = NOW + x * LATER / MI; c < NOW + (x + 1) * LATER / MI; ++c)
+                    copy_code(c, 2 * chunk + P - 1 + R, pair == 0 ? R - 1 : pair - 1);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -579,7 +588,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
 
 // Joins the parts of k: out = [out +] the sum of `splits` float32 matrices m x n
 // (rows ldp entries apart), added in order, so that every run gives the same bits.
-// 1024 x 1024 x 32768 takes 32 us with its join, 63 in one part.
+// 1024 x 1024 x 32768 takes 31 us with its join, 63 in one part.
 template <bool BF16>
 __global__ __launch_bounds__(256) void mxfp4_join(const float* parts, int splits, long long split_floats, int m, int n, int ldp,
                                                   void* out, long long ldo, bool add) {
