@@ -129,6 +129,7 @@ struct Eight<false> {
 template <bool BF16, int N>
 __device__ __forceinline__ void load_out(const void* p, long long at, float (&v)[N]) {
     constexpr int M = BF16 ? 8 : 4;
+    static_assert(N % M == 0, "whole accesses");
     const u32x4_any* from = reinterpret_cast<const u32x4_any*>(reinterpret_cast<const char*>(p) + at * (BF16 ? 2 : 4));
 #pragma unroll
     for (int o = 0; o < N; o += M) {
@@ -147,6 +148,7 @@ __device__ __forceinline__ void load_out(const void* p, long long at, float (&v)
 template <bool BF16, int N>
 __device__ __forceinline__ void store_out(void* p, long long at, const float (&v)[N]) {
     constexpr int M = BF16 ? 8 : 4;
+    static_assert(N % M == 0, "whole accesses");
     u32x4_any* to = reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(p) + at * (BF16 ? 2 : 4));
 #pragma unroll
     for (int o = 0; o < N; o += M) {
@@ -524,8 +526,10 @@ void launch_decode(const uint8_t* codes, const uint8_t* scales, int nmsg, long l
     };
     // One message to float32 is bound by its stores (whole lines with four entries a
     // thread: 17.6 against 28 us for 25.6M entries), several by their loads.
-    if (BF16 || nmsg > 1) go(std::integral_constant<int, 8>{});
-    else go(std::integral_constant<int, 4>{});
+    if constexpr (!BF16) {
+        if (nmsg == 1) return go(std::integral_constant<int, 4>{});
+    }
+    go(std::integral_constant<int, 8>{});
 }
 
 }  // namespace
