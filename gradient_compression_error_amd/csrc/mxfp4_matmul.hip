@@ -274,12 +274,13 @@ __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
 }
 
-// Waits until at most N of this wave's LDS reads are outstanding.
-template <int N>
-__device__ __forceinline__ void wait_reads() {
-    static_assert(N >= 0 && N < 16, "lgkmcnt has four bits");
-    asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(N) : "memory");
-}
+// Waits until all of this wave's LDS reads are back.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Uses a value that was read from LDS, so that the compiler waits for that read here,
+// counting the ones issued since by itself.
+template <typename T>
+__device__ __forceinline__ void arrived(const T& v) { asm volatile("" ::"v"(v) : "memory"); }
 
 // Workgroup tile BM x BN of out over one part of k, waves WM x WN.  Stages of 128
 // columns of k (one group) are copied to LDS in pairs, R pairs at a time; a wave
@@ -467,7 +468,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
         const Place next = {G ? pair1 : pair, P && G ? ring1 : ring, 1 - G, (2 * P + G + 1) & 3};
         if constexpr (G == 1) {
             wait_for<(R - 2) * (CP + SP / 2)>();            // the next pair has landed
-            if constexpr (EARLY) wait_reads<0>();           // (issued a stage ago) and nobody reads this one any more
+            if constexpr (EARLY) wait_reads();              // (issued a stage ago) and nobody reads this one any more
             meet();
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -493,11 +494,14 @@ __global__ __launch_bounds__(WM* WN * 64) void mxfp4_tile(const Operand A, const
             }
             if constexpr (G == 1) {
                 if (!EARLY && x == 0) {
-                    // all but the six reads above (two fragments, two scale words)
-                    // are back, so once every wave is here nobody reads this pair
-                    // any more
+                    // all of this stage's fragments are here (the next one's reads, six
+                    // so far, may still be out), so once every wave is here nobody reads
+                    // this pair any more
                     __builtin_amdgcn_sched_barrier(0);
-                    wait_reads<6>();
+#pragma unroll
+                    for (int z = MI - 1; z >= 1; --z) arrived(sa[z]), arrived(fa[z][1]), arrived(fa[z][0]);
+#pragma unroll
+                    for (int z = NI - 1; z >= 0; --z) arrived(sb[z]), arrived(fb[z][1]), arrived(fb[z][0]);
                     meet();
                 } else {
                     constexpr int FROM = EARLY ? 0 : 1;
