@@ -615,6 +615,8 @@ def gc_mxfp4_decode(codes, scales, out, weight: float = 1.0, accumulate: bool = 
         nmsg = codes.shape[0]
         if nmsg < 1 or scales.shape[0] != nmsg:
             raise ValueError("codes and scales need one row per message")
+        if nmsg > 1 << 20:                                  # the C call takes an int
+            raise ValueError("a call takes at most 2^20 messages")
         units = rows * ((cols + 127) >> 7)
         if codes.shape[1] < 64 * units:
             raise ValueError("codes need gc_mxfp4_code_bytes entries a message")
