@@ -1,0 +1,50 @@
+"""GPU: the MXFP4 product's kernels on the paths that few or shallow sums do not reach, and the operators together.
+
+Products are compared exactly where no order of the additions rounds: with scale bytes in [low, high] every term is a
+whole multiple of 2^-2 * 2^(2 (low - 127)) and at most 36 * 2^(2 (high - 127)), so a sum of K terms is exact in float32
+for 144 * K * 4^(high - low) < 2^24.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gen
+import oracle
+from gpu_util import DEV, f32_bits, lib, rel_err, require_gpu, to_dev
+from test_gpu_mxfp4 import Held, held_from, linear_setup, product, random_held, same, sums32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def rng(which, m=0, n=0, k=0):
+    return gen.rng(0, gen.KIND_MISC, 700 + which, m * 31 + n * 7 + k)
+
+
+# Outs that take the 256 x 256 tile, the 128 x 128 tile with two on a compute unit, that tile alone, and in parts of k.
+# A place for scales in LDS is first read after it was written again from group 13, 13 and 17 of 128 columns on; the
+# groups past the last whole four are 0 to 3.
+DEEP = [(4000, 3970, 3000), (4000, 3970, 3100), (4000, 3970, 3300), (3841, 4095, 3400),
+        (2100, 2000, 1650), (2100, 2000, 1700), (2049, 2100, 1900), (2100, 2000, 2000),
+        (700, 900, 2100), (700, 900, 2200), (700, 900, 2400), (700, 900, 2500),
+        (385, 641, 14400)]
+
+
+@pytest.mark.parametrize("m,n,k", DEEP)
+def test_deep_product_exact(m, n, k):
+    """Three scales within a factor of four (144 * 3400 * 16 < 2^24; two for the deepest: 144 * 14400 * 4 < 2^24)."""
+    print(f"case: mxfp4 matmul deep {m}x{n}x{k}", flush=True)
+    r = rng(1, m, n, k)
+    low = 125 if k < 7000 else 126
+    a, b = random_held(r, m, k, low, 127), random_held(r, n, k, low, 127)
+    want = torch.from_numpy(oracle.mxfp4_matmul(a, b, k).astype(np.float32))
+    assert torch.equal(product(a, b, m, n, k), want)
+    assert torch.equal(product(a, b, m, n, k, dtype=torch.bfloat16, pitch=n + 6), want.to(torch.bfloat16))
+    old = torch.from_numpy(r.integers(-1000, 1000, (m, n)).astype(np.float32))
+    assert torch.equal(product(a, b, m, n, k, old=old.numpy()), want + old)
+    old16 = old.to(torch.bfloat16)
+    assert torch.equal(product(a, b, m, n, k, dtype=torch.bfloat16, old=old16.float().numpy()), (want + old16.float()).to(torch.bfloat16))
