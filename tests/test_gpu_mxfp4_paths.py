@@ -48,3 +48,59 @@ def test_deep_product_exact(m, n, k):
     assert torch.equal(product(a, b, m, n, k, old=old.numpy()), want + old)
     old16 = old.to(torch.bfloat16)
     assert torch.equal(product(a, b, m, n, k, dtype=torch.bfloat16, old=old16.float().numpy()), (want + old16.float()).to(torch.bfloat16))
+
+
+# One out for each tile of the product, and one in parts of k; the first for the kernel of few tiles.
+TILES = [(300, 300, 512), (700, 900, 2100), (300, 520, 16384), (2100, 2000, 1000), (4000, 3970, 1700)]
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_scale_ends_on_every_tile(m, n, k):
+    """The least and the largest scale against each other: the terms are those of scales 2^0 and 2^0 (their scale bytes
+    add up to 254), 144 * K < 2^24."""
+    print(f"case: mxfp4 matmul scale ends {m}x{n}x{k}", flush=True)
+    r = rng(2, m, n, k)
+    a, b = random_held(r, m, k, 127, 127), random_held(r, n, k, 127, 127)
+    want = torch.from_numpy(oracle.mxfp4_matmul(a, b, k).astype(np.float32))
+    blocks = -(-k // 32)
+    for sa, sb in [(0, 254), (254, 0)]:
+        a[1][:, :blocks], b[1][:, :blocks] = sa, sb
+        assert torch.equal(product(a, b, m, n, k), want)
+    # by blocks: byte s against 254 - s
+    s = r.integers(0, 255, blocks).astype(np.uint8)
+    a[1][:, :blocks], b[1][:, :blocks] = s, 254 - s
+    assert torch.equal(product(a, b, m, n, k), want)
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_nan_scales_on_every_tile(m, n, k):
+    """A NaN scale in the first and the last block of a row makes that row (or column) of out NaN, zero codes or not, and
+    nothing else."""
+    print(f"case: mxfp4 matmul NaN scales {m}x{n}x{k}", flush=True)
+    r = rng(3, m, n, k)
+    a, b = random_held(r, m, k, 127, 127), random_held(r, n, k, 127, 127)
+    want = torch.from_numpy(oracle.mxfp4_matmul(a, b, k).astype(np.float32))
+    last = (k - 1) // 32
+    bad = torch.zeros(m, n, dtype=torch.bool)
+    for row, block in [(0, last), (m // 2, last // 2), (m - 1, 0)]:
+        a[1][row, block] = 255
+        bad[row] = True
+    for col, block in [(1, 0), (n // 3, last), (n - 1, last)]:
+        b[1][col, block] = 255
+        bad[:, col] = True
+    a[0][0, last * 16:last * 16 + 16] = 0
+    b[0][1, :16] = 0
+    got = product(a, b, m, n, k)
+    assert bool(got[bad].isnan().all())
+    assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_bound_on_every_tile(m, n, k):
+    """Scales over 24 binades, so that the sums round: at most one last place of the magnitudes' sum an addition."""
+    print(f"case: mxfp4 matmul bound {m}x{n}x{k}", flush=True)
+    r = rng(4, m, n, k)
+    a, b = random_held(r, m, k, 110, 133), random_held(r, n, k, 110, 133)
+    va, vb = oracle.mxfp4_values(*a, k), oracle.mxfp4_values(*b, k)
+    err = np.abs(product(a, b, m, n, k).numpy() - va @ vb.T)
+    assert np.all(err <= k * 2.0 ** -23 * (np.abs(va) @ np.abs(vb).T))
