@@ -104,3 +104,19 @@ def test_bound_on_every_tile(m, n, k):
     va, vb = oracle.mxfp4_values(*a, k), oracle.mxfp4_values(*b, k)
     err = np.abs(product(a, b, m, n, k).numpy() - va @ vb.T)
     assert np.all(err <= k * 2.0 ** -23 * (np.abs(va) @ np.abs(vb).T))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 64, 256), (20, 40, 300), (300, 300, 512), (600, 512, 4096)] + TILES[1:])
+def test_least_scales_exact(m, n, k):
+    """Terms below float32's least normal value are kept: with scales 2^-127 and 2^b they are whole multiples of
+    2^(b - 129), which float32 holds down to 2^-149, and a sum of K is exact for 144 * K < 2^24."""
+    print(f"case: mxfp4 matmul least scales {m}x{n}x{k}", flush=True)
+    r = rng(5, m, n, k)
+    a, b = random_held(r, m, k, 127, 127), random_held(r, n, k, 127, 127)
+    blocks = -(-k // 32)
+    a[1][:, :blocks] = 0
+    for power in (0, -10, -20):
+        b[1][:, :blocks] = 127 + power
+        want = oracle.mxfp4_matmul(a, b, k)
+        assert np.abs(want).max() >= 2.0 ** (power - 126)
+        assert np.array_equal(product(a, b, m, n, k).numpy().astype(np.float64), want)

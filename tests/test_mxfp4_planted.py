@@ -25,3 +25,14 @@ def test_stale_scales_are_noticed(places):
         first, last = chunk * 16, min(chunk * 16 + 16, b[1].shape[1])
         stale[:, first:last] = b[1][:, first - places * 16:last - places * 16]
         assert np.mean(oracle.mxfp4_matmul(a, (b[0], stale), K) != want) > 0.9
+
+
+def test_dropped_small_terms_are_noticed():
+    """At the least scale: a product that takes all terms, or the terms below 2^-126, as zero."""
+    a, b = operands(127, 127)
+    a[1][:, : -(-K // 32)] = 0
+    want = oracle.mxfp4_matmul(a, b, K)
+    va, vb = oracle.mxfp4_values(*a, K), oracle.mxfp4_values(*b, K)
+    terms = va[:, None, :] * vb[None, :, :]
+    flushed = np.where(np.abs(terms) < 2.0 ** -126, 0.0, terms).sum(2)
+    assert np.mean(want != 0) > 0.9 and np.mean(flushed != want) > 0.9
