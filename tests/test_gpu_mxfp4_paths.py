@@ -120,3 +120,28 @@ def test_least_scales_exact(m, n, k):
         want = oracle.mxfp4_matmul(a, b, k)
         assert np.abs(want).max() >= 2.0 ** (power - 126)
         assert np.array_equal(product(a, b, m, n, k).numpy().astype(np.float64), want)
+
+
+def test_products_in_turn_on_one_workspace():
+    """Two products in parts of k, another number and size of them, on one workspace in turn: what one left there does
+    not reach the other's result."""
+    gc = lib()
+    shapes = [(256, 512, 16384), (385, 641, 14400)]
+    need = [gc.gc_mxfp4_matmul_workspace_bytes(*s) for s in shapes]
+    assert min(need) > 0
+    ws = torch.full((max(need),), 0xFF, dtype=torch.uint8, device=DEV)
+    r = rng(6)
+    held, want = [], []
+    for m, n, k in shapes:
+        a, b = random_held(r, m, k, 126, 127), random_held(r, n, k, 126, 127)
+        held.append((held_from(*a), held_from(*b)))
+        want.append(torch.from_numpy(oracle.mxfp4_matmul(a, b, k).astype(np.float32)))
+    outs = []
+    for i in (0, 1, 0, 0, 1):
+        m, n, k = shapes[i]
+        print(f"case: mxfp4 matmul in turn {m}x{n}x{k}", flush=True)
+        out = torch.empty(m, n, device=DEV)
+        gc.gc_mxfp4_matmul(*held[i][0], *held[i][1], k, out, ws)
+        outs.append((i, out))
+    for i, out in outs:
+        assert torch.equal(out.cpu(), want[i])
