@@ -145,3 +145,63 @@ def test_products_in_turn_on_one_workspace():
         outs.append((i, out))
     for i, out in outs:
         assert torch.equal(out.cpu(), want[i])
+
+
+def test_product_in_parts_on_a_side_stream_and_in_graphs():
+    """A weight's gradient over many tokens, its product in parts of k (a workspace for each user): on another stream,
+    then in two graphs that are replayed with eager work between; every result equals the eager one bit for bit."""
+    gc = lib()
+    t, fi, fo = 16384, 512, 256
+    print(f"case: mxfp4 product in parts, side stream and graphs {fo}x{fi}x{t}", flush=True)
+    assert gc.gc_mxfp4_matmul_workspace_bytes(fo, fi, t) > 0
+    x, _, dy = linear_setup(t, fi, fo)
+
+    class Layer:
+        def __init__(self):
+            self.x, self.dy = torch.empty(t, fi, device=DEV), torch.empty(t, fo, device=DEV)
+            self.xc, self.dyc = Held(fi, t), Held(fo, t)
+            self.dw = torch.zeros(fo, fi, device=DEV)
+            self.ws = torch.empty(gc.gc_mxfp4_matmul_workspace_bytes(fo, fi, t), dtype=torch.uint8, device=DEV)
+
+        def load(self, step):
+            self.x.copy_(to_dev(np.roll(x, step, 0)))
+            self.dy.copy_(to_dev(dy * np.float32(1 + step)))
+            self.dw.fill_(0.25)
+
+        def run(self):
+            gc.gc_mxfp4_quantize(self.x, None, None, *self.xc.pair)
+            gc.gc_mxfp4_quantize(self.dy, None, None, *self.dyc.pair)
+            gc.gc_mxfp4_matmul(*self.dyc.pair, *self.xc.pair, t, self.dw, self.ws, accumulate=True)
+
+    eager, steps = Layer(), []
+    for s in range(4):
+        eager.load(s)
+        eager.run()
+        steps.append(f32_bits(eager.dw))
+    va, vb = (oracle.mxfp4_values(*h.host(), t) for h in (eager.dyc, eager.xc))
+    err = np.abs(eager.dw.cpu().numpy() - (va @ vb.T + 0.25))
+    assert np.all(err <= (t + 1) * 2.0 ** -23 * (np.abs(va) @ np.abs(vb).T + 0.25))
+    side, other = torch.cuda.Stream(), Layer()
+    for s in range(4):
+        other.load(s)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other.run()
+        torch.cuda.current_stream().wait_stream(side)
+        assert np.array_equal(f32_bits(other.dw), steps[s])
+    graphs = []
+    for _ in range(2):
+        layer = Layer()
+        layer.load(0)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            layer.run()
+        graphs.append((g, layer))
+    for s in range(4):
+        for g, layer in graphs:
+            layer.load(s)
+            g.replay()
+        torch.ones(1000, device=DEV).sum().item()
+        for _, layer in graphs:
+            assert np.array_equal(f32_bits(layer.dw), steps[s])
