@@ -205,3 +205,55 @@ def test_product_in_parts_on_a_side_stream_and_in_graphs():
         torch.ones(1000, device=DEV).sum().item()
         for _, layer in graphs:
             assert np.array_equal(f32_bits(layer.dw), steps[s])
+
+
+def test_layer_gradients_exchanged():
+    """Four workers: a layer's weight gradient from MXFP4 products over two micro-batches, its message with memory, the
+    gathered messages' mean, for two steps; and the same gradient through PowerSGD with memory."""
+    gc = lib()
+    workers, t, fi, fo, eta = 4, 96, 160, 72, 0.5
+    print(f"case: mxfp4 layer gradients of {workers} workers {t}x{fi}x{fo}", flush=True)
+    d = fo * fi
+    nc, ns = gc.gc_mxfp4_code_bytes(1, d), gc.gc_mxfp4_scale_bytes(1, d)
+    x, _, dy = linear_setup(t, fi, fo)
+    mems = [torch.zeros(d, device=DEV) for _ in range(workers)]
+    host_mems = [np.zeros(d, np.float32) for _ in range(workers)]
+    gathered = torch.full((workers, -(-(nc + ns) // 16) * 16), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(max(16, gc.gc_mxfp4_matmul_workspace_bytes(fo, fi, t)), dtype=torch.uint8, device=DEV)
+    mean = torch.empty(d, device=DEV)
+    for step in range(2):
+        codes, scales = [], []
+        for w in range(workers):
+            dw = torch.zeros(fo, fi, device=DEV)
+            total, size = np.zeros((fo, fi)), np.zeros((fo, fi))
+            for micro in range(2):
+                shift = 8 * step + 2 * w + micro
+                xh, dyh = np.roll(x, shift, 0), np.roll(dy, 3 * shift, 1)
+                xc, dyc = Held(fi, t), Held(fo, t)
+                gc.gc_mxfp4_quantize(to_dev(xh), None, None, *xc.pair)
+                gc.gc_mxfp4_quantize(to_dev(dyh), None, None, *dyc.pair)
+                same(xc, oracle.mxfp4_quantize(np.ascontiguousarray(xh.T)))
+                same(dyc, oracle.mxfp4_quantize(np.ascontiguousarray(dyh.T)))
+                gc.gc_mxfp4_matmul(*dyc.pair, *xc.pair, t, dw, ws, accumulate=True)
+                va, vb = oracle.mxfp4_values(*dyc.host(), t), oracle.mxfp4_values(*xc.host(), t)
+                total, size = total + va @ vb.T, size + np.abs(va) @ np.abs(vb).T
+            # t additions a micro-batch, and one to what was there
+            assert np.all(np.abs(dw.cpu().numpy() - total) <= 2 * (t + 1) * 2.0 ** -23 * size)
+            message = gathered[w, :nc], gathered[w, nc:nc + ns]
+            gc.gc_mxfp4_ef_encode(dw.view(-1), mems[w], eta, *message)
+            ref = oracle.mxfp4_ef_step(host_mems[w], dw.cpu().numpy().ravel(), eta)
+            assert np.array_equal(message[0].cpu().numpy(), ref["codes"][0]) and np.array_equal(message[1].cpu().numpy(), ref["scales"][0])
+            assert np.array_equal(f32_bits(mems[w]), f32_bits(ref["mem"]))
+            host_mems[w] = ref["mem"]
+            codes.append(ref["codes"])
+            scales.append(ref["scales"])
+        gc.gc_mxfp4_decode(gathered[:, :nc], gathered[:, nc:nc + ns], mean, weight=1.0 / workers)
+        assert np.array_equal(f32_bits(mean), f32_bits(sums32(codes, scales, d, 1.0 / workers, None).ravel()))
+    # the last worker's gradient as a matrix of a low-rank step
+    mem, q, out = torch.zeros(fo, fi, device=DEV), to_dev(gen.q_init(0, 0, fi)), torch.zeros(fo, fi, device=DEV)
+    q_before = q.cpu().numpy()
+    mats = [gc.Mat(grad=dw, mem=mem, q=q, rank=2, p=torch.zeros(4, fo, device=DEV), out=out)]
+    gc.gc_powersgd_ef_step(mats, eta, torch.empty(gc.gc_powersgd_workspace_bytes(mats), dtype=torch.uint8, device=DEV))
+    ref = oracle.powersgd_ef_step(dw.cpu().numpy(), np.zeros((fo, fi), np.float32), q_before.T, eta, 2)
+    # the low-rank step's tolerance: float32 sums of at most 160 terms, twice over, through a well-conditioned P
+    assert rel_err(out.cpu().numpy(), ref["out"]) <= 1e-4 and rel_err(mem.cpu().numpy(), ref["mem"]) <= 1e-4
