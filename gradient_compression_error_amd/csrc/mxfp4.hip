@@ -252,7 +252,9 @@ __global__ __launch_bounds__(MX_THREADS) void mxfp4_ef(const void* grad, float* 
 }
 
 // Quantisation along the rows.  A thread takes eight columns, four lanes a block, so
-// that a wave reads 1 KiB of bf16 together.  8192 x 4096 bf16: 14.2 us, 6.0 TB/s.
+// that a wave reads 1 KiB of bf16 together.  8192 x 4096 bf16: 14.2 us, 6.0 TB/s;
+// float32, whose 32 bytes a thread are two loads that each pass over every other 16: 27.5 us,
+// 5.5 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(MX_THREADS) void mxfp4_rows(const void* x, long long ld, long long units, unsigned per_row,
                                                          long long cols, unsigned* codes, unsigned* scales) {
@@ -283,8 +285,9 @@ __global__ __launch_bounds__(MX_THREADS) void mxfp4_rows(const void* x, long lon
 // bytes.  The words meet in LDS, at places that keep the banks apart, and leave 16
 // bytes a lane, 64 of a row or column together: stored word by word they took 11 of 29
 // us (8192 x 4096 bf16, both forms).  Both take 25.7 us now, 4.0 TB/s (a kernel for
-// each: 58), the columns alone 14.6: what the second form adds is its conversions and
-// its way through LDS.  Tiles go down four and along on an XCD, since
+// each: 58), the columns alone 14.6.  float32: 42.5 us and 38.5, 4.0 TB/s.  For both forms
+// of bf16 ten waves fit a compute unit and wait, for memory and each other, 58% of their
+// time; LDS is busy for 11% of it.  Tiles go down four and along on an XCD, since
 // neighbours share lines of either form's codes and scales.
 template <bool BF16, bool ROWS>
 __global__ __launch_bounds__(MX_THREADS) void mxfp4_cols(const void* x, long long ld, long long rows, long long cols,
@@ -413,7 +416,8 @@ __global__ __launch_bounds__(MX_THREADS) void mxfp4_cols(const void* x, long lon
 // out = [out +] weight * sum over the messages of their values, added in message
 // order in float32 and rounded once to the output type.  A thread writes 16 bytes (32
 // to float32 from several messages); four messages' codes are in flight at a time.
-// 25.6M float32 entries of one message: 17.6 us, 6.6 TB/s.
+// 25.6M float32 entries of one message: 17.5 us, 6.6 TB/s; added to what is there 33.9,
+// 6.4 TB/s.
 template <bool BF16, bool ADD, bool FLAT, int N>
 __global__ __launch_bounds__(MX_THREADS) void mxfp4_decode(const unsigned char* codes, const unsigned char* scales,
                                                            int nmsg, long long code_stride, long long scale_stride,
@@ -525,7 +529,7 @@ void launch_decode(const uint8_t* codes, const uint8_t* scales, int nmsg, long l
             mxfp4_decode<BF16, ADD, false, N><<<grid, MX_THREADS, 0, s>>>(codes, scales, nmsg, cstride, sstride, units, pr, cols, weight, out);
     };
     // One message to float32 is bound by its stores (whole lines with four entries a
-    // thread: 17.6 against 28 us for 25.6M entries), several by their loads.
+    // thread: 17.5 against 28 us for 25.6M entries), several by their loads.
     if constexpr (!BF16) {
         if (nmsg == 1) return go(std::integral_constant<int, 4>{});
     }

@@ -6,12 +6,14 @@
 // one block, and the block's scale byte.  B goes in as the first operand, so that a
 // lane's results are neighbours in a row of out.
 //
-// What bounds it: for large products the chip's power (8192^3 with random codes:
-// 260 us, 4.2 PFLOP/s; 211 without the copies from memory, 158 with codes of zero); for
-// about one 128 x 128 tile a compute unit the copies into LDS and the matrix
-// instructions, which overlap in part (4096 x 1024 x 8192: 23.8 us, either alone about
-// 15); for few rows the read of B (16 x 8192 x 8192: 10.0 us, 3.6 TB/s); for small
-// calls the launch (1 x 4096 x 1024: 2.6 us).
+// What bounds it.  Large products: 8192^3 with random codes takes 266 us (4.1 PFLOP/s),
+// the matrix units busy for 59% of the cycles and the clock lowered to 1.7 GHz by the
+// chip's power (158 us with codes of zero, 211 without the copies from memory).  About one
+// 128 x 128 tile a compute unit: the copies into LDS and the matrix instructions, which
+// overlap in part (4096 x 1024 x 8192: 25.0 us, either alone about 15; matrix units busy
+// for 42% of the cycles).  Few rows: waiting for the read of B, two units of k one after
+// the other (16 x 8192 x 8192: 10.0 us, 3.6 TB/s; one row 8.4; the waves wait for 60% of
+// their time).  Small calls: the launch (1 x 4096 x 1024: 2.5 us).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -292,8 +294,9 @@ __device__ __forceinline__ void arrived(const T& v) { asm volatile("" ::"v"(v) :
 //   256 x 256, four waves of 128 x 128, R = 2: every operand byte read from LDS serves
 //       128 rows, and a lane holds 256 accumulators; with eight waves 290 against 278 us.
 //   128 x 128, eight waves of 64 x 32, R = 4: a compute unit for each of up to 256 tiles.
-//       4096 x 1024 x 8192: 23.8 us, 30.9 with the next, 48.8 with the first; 25.5 with
-//       two teams of four 64 x 64 waves that share k, which read a third less from LDS.
+//       4096 x 1024 x 8192: 23.8 us (25.0 on other cards), 30.9 with the next, 48.8 with the
+//       first; 25.5 with two teams of four 64 x 64 waves that share k, which read a third
+//       less from LDS.
 //   128 x 128, four waves of 64 x 64, R = 2: two tiles a compute unit for more than 256.
 //       4096 x 2048 x 8192: 43.8 us, 51.8 with the one before, 53.0 with the first.
 //

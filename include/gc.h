@@ -10,7 +10,9 @@
  *     utility-of-compression paper's method/results sections),
  *   - the per-layer gradient norms and the two-level switch of Accordion
  *     (Accordion paper, method section: l_low / l_high chosen from the rate of
- *     change of the gradient norm).
+ *     change of the gradient norm),
+ *   - MXFP4 (microscaled 4-bit floating point): the compressor with memory, the
+ *     decode of gathered messages, the quantisation and the product of matrices.
  *
  * Conventions shared by every entry point
  *   - Tensor pointers are DEVICE pointers owned by the caller unless marked
@@ -27,7 +29,8 @@
  *     work is enqueued, so a call that fails validation changes no buffer.
  *     gc_last_error() gives a message for the last failure on this thread.
  *   - Gradients may be float32 (GC_F32) or bfloat16 (GC_BF16); memory, factors
- *     and decoded outputs are always float32.
+ *     and decoded outputs are always float32, except that gc_mxfp4_decode and
+ *     gc_mxfp4_matmul write either type (out_dtype).
  *   - Results are deterministic: the same inputs give the same bits on every
  *     call (all reductions have a fixed order; no floating-point atomics).
  *   - Calls that share a workspace must not overlap in time (use one stream).
@@ -393,8 +396,8 @@ size_t gc_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
  *     out[i, j] = [out[i, j] +] sum_k D(A)[i, k] * D(B)[j, k]
  * A is m x k, B is n x k; out has m rows of n entries, ldo entries apart
  * (ldo >= n, (m - 1) ldo <= 2^40), float32 or bf16 (out_dtype).  Products are summed in float32 in
- * an order fixed by the sizes; out is rounded once.  Entries of out between
- * the rows (n .. ldo) are left alone.
+ * an order fixed by the sizes, values below float32's least normal one included;
+ * out is rounded once.  Entries of out between the rows (n .. ldo) are left alone.
  *   m, n     in [1, 2^30], k in [1, 2^24]; each matrix, and m x n, within the
  *            range above
  *   ws       >= gc_mxfp4_matmul_workspace_bytes(m, n, k) bytes (may be NULL for 0)
