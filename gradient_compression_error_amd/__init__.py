@@ -82,6 +82,12 @@ _sig("gc_mxfp4_decode", _i32, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _f32, _vp,
 _sig("gc_mxfp4_quantize", _i32, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp)
 _sig("gc_mxfp4_matmul_workspace_bytes", _sz, _i64, _i64, _i64)
 _sig("gc_mxfp4_matmul", _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i32, _i32, _vp, _sz, _vp)
+_sig("gc_fp8_code_bytes", _sz, _i64, _i64)
+_sig("gc_fp8_scale_bytes", _sz, _i64, _i64, _i32)
+_sig("gc_fp8_quantize", _i32, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp)
+_sig("gc_fp8_dequantize", _i32, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _i32, _vp)
+_sig("gc_fp8_matmul_workspace_bytes", _sz, _i64, _i64, _i64)
+_sig("gc_fp8_matmul", _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i64, _i32, _i32, _vp, _sz, _vp)
 _sig("gc_timing_enable", _i32, C.c_char_p)
 _sig("gc_timing_read", _i32, C.POINTER(C.c_double), C.POINTER(C.c_int64))
 _sig("gc_kernel_names", C.c_char_p)
@@ -95,6 +101,8 @@ EXPORTED = ["gc_status_str", "gc_last_error", "gc_topk_workspace_bytes", "gc_top
             "gc_accordion_select",
             "gc_mxfp4_code_bytes", "gc_mxfp4_scale_bytes", "gc_mxfp4_ef_encode", "gc_mxfp4_decode",
             "gc_mxfp4_quantize", "gc_mxfp4_matmul_workspace_bytes", "gc_mxfp4_matmul",
+            "gc_fp8_code_bytes", "gc_fp8_scale_bytes", "gc_fp8_quantize", "gc_fp8_dequantize",
+            "gc_fp8_matmul_workspace_bytes", "gc_fp8_matmul",
             "gc_timing_enable", "gc_timing_read", "gc_kernel_names"]
 
 
@@ -679,6 +687,96 @@ def gc_mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, k: int, out, ws=None, 
         pw, wb = ws.data_ptr(), ws.nbytes
     _mx_call(dev, stream, "gc_mxfp4_matmul", lib.gc_mxfp4_matmul,
              (pac, pas, pbc, pbs, m, n, k, out.data_ptr(), ldo, _mx_dtype(out, "out"), 1 if accumulate else 0, pw, wb))
+
+
+# ------------------------------------------------------------------ 8-bit floating point
+
+def gc_fp8_code_bytes(rows: int, cols: int) -> int:
+    return int(lib.gc_fp8_code_bytes(rows, cols))
+
+
+def gc_fp8_scale_bytes(rows: int, cols: int, block_rows: int = 1) -> int:
+    return int(lib.gc_fp8_scale_bytes(rows, cols, block_rows))
+
+
+def _f8_held(codes, scales, rows: int, cols: int, block_rows: int, dev: int, name: str):
+    """Addresses of an 8-bit matrix's two buffers: uint8, contiguous, with room for the shape, on device dev."""
+    if codes.dtype is not _u8 or scales.dtype is not _u8:
+        raise TypeError(f"{name} codes and scales: expected torch.uint8, got {codes.dtype} and {scales.dtype}")
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError("block rows must be 1 or 128")
+    groups = (cols + 127) >> 7
+    if codes.numel() < 128 * groups * rows:
+        raise ValueError(f"{name} codes need gc_fp8_code_bytes entries")
+    if scales.numel() < (rows if block_rows == 1 else (rows + 127) >> 7) * ((groups + 3) & ~3):
+        raise ValueError(f"{name} scales need gc_fp8_scale_bytes entries")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    if codes.get_device() != dev:
+        _mx_elsewhere(codes)
+    if scales.get_device() != dev:
+        _mx_elsewhere(scales)
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def gc_fp8_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, block_rows: int = 1, stream=None) -> None:
+    """Q8 of a matrix along its rows (codes, scales: rows x cols), along its columns
+    (codes_t, scales_t: cols x rows, transposed), or both, in blocks of 1 or 128 rows by
+    128 columns.  x may be a view with a row pitch."""
+    if _torch is None:
+        _mx_load()
+    rows, cols, ld = _mx_pitched(x, "x")
+    if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
+        raise ValueError("a form needs codes and scales")
+    dev = x.get_device()
+    pc = ps = pct = pst = None
+    if codes is not None:
+        pc, ps = _f8_held(codes, scales, rows, cols, block_rows, dev, "row")
+    if codes_t is not None:
+        pct, pst = _f8_held(codes_t, scales_t, cols, rows, block_rows, dev, "column")
+    if pc is None and pct is None:
+        raise ValueError("no output given")
+    _mx_call(dev, stream, "gc_fp8_quantize", lib.gc_fp8_quantize,
+             (x.data_ptr(), _mx_dtype(x, "x"), rows, cols, ld, block_rows, pc, ps, pct, pst))
+
+
+def gc_fp8_dequantize(codes, scales, out, block_rows: int = 1, stream=None) -> None:
+    """The values of an 8-bit matrix of out's shape, in out (float32 or bf16; may be a view with a row pitch)."""
+    if _torch is None:
+        _mx_load()
+    rows, cols, ldo = _mx_pitched(out, "out")
+    dev = out.get_device()
+    pc, ps = _f8_held(codes, scales, rows, cols, block_rows, dev, "matrix")
+    _mx_call(dev, stream, "gc_fp8_dequantize", lib.gc_fp8_dequantize,
+             (pc, ps, block_rows, rows, cols, out.data_ptr(), ldo, _mx_dtype(out, "out")))
+
+
+def gc_fp8_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(lib.gc_fp8_matmul_workspace_bytes(m, n, k))
+
+
+def gc_fp8_matmul(a_codes, a_scales, b_codes, b_scales, k: int, out, ws=None, a_block_rows: int = 1,
+                  b_block_rows: int = 1, accumulate: bool = False, stream=None) -> None:
+    """out [m, n] = [out +] A B^T for 8-bit matrices A (m x k) and B (n x k); out may be a view with a row pitch."""
+    if _torch is None:
+        _mx_load()
+    m, n, ldo = _mx_pitched(out, "out")
+    k = int(k)
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    dev = out.get_device()
+    pac, pas = _f8_held(a_codes, a_scales, m, k, a_block_rows, dev, "A")
+    pbc, pbs = _f8_held(b_codes, b_scales, n, k, b_block_rows, dev, "B")
+    pw, wb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev:
+            _mx_elsewhere(ws)
+        if not ws.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        pw, wb = ws.data_ptr(), ws.nbytes
+    _mx_call(dev, stream, "gc_fp8_matmul", lib.gc_fp8_matmul,
+             (pac, pas, a_block_rows, pbc, pbs, b_block_rows, m, n, k, out.data_ptr(), ldo, _mx_dtype(out, "out"),
+              1 if accumulate else 0, pw, wb))
 
 
 # ------------------------------------------------------------------ timing hooks

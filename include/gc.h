@@ -12,7 +12,9 @@
  *     (Accordion paper, method section: l_low / l_high chosen from the rate of
  *     change of the gradient norm),
  *   - MXFP4 (microscaled 4-bit floating point): the compressor with memory, the
- *     decode of gathered messages, the quantisation and the product of matrices.
+ *     decode of gathered messages, the quantisation and the product of matrices,
+ *   - 8-bit floating point with a scale for each block of 128: the quantisation
+ *     and the product of matrices.
  *
  * Conventions shared by every entry point
  *   - Tensor pointers are DEVICE pointers owned by the caller unless marked
@@ -29,8 +31,9 @@
  *     work is enqueued, so a call that fails validation changes no buffer.
  *     gc_last_error() gives a message for the last failure on this thread.
  *   - Gradients may be float32 (GC_F32) or bfloat16 (GC_BF16); memory, factors
- *     and decoded outputs are always float32, except that gc_mxfp4_decode and
- *     gc_mxfp4_matmul write either type (out_dtype).
+ *     and decoded outputs are always float32, except that gc_mxfp4_decode,
+ *     gc_mxfp4_matmul, gc_fp8_dequantize and gc_fp8_matmul write either type
+ *     (out_dtype).
  *   - Results are deterministic: the same inputs give the same bits on every
  *     call (all reductions have a fixed order; no floating-point atomics).
  *   - Calls that share a workspace must not overlap in time (use one stream).
@@ -408,6 +411,88 @@ size_t gc_mxfp4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int gc_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
                     int64_t m, int64_t n, int64_t k, void* out, int64_t ldo, int out_dtype, int accumulate, void* ws,
                     size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit floating point in blocks of 128                                     */
+/* ------------------------------------------------------------------------ */
+
+/* An 8-bit matrix of rows x cols entries is two device buffers.  Each row is
+ * held in G = ceil(cols / 128) groups of 128 columns:
+ *   codes   rows x 128 G bytes: E4M3 codes (sign, four exponent bits, three
+ *           mantissa bits; largest magnitude 448, no infinity, 0x7F is NaN);
+ *   scales  one E8M0 byte s a block, standing for 2^(s - 127); 255 is NaN, and
+ *           every value of its block is NaN.  block_rows says what a block is:
+ *             1    128 columns of one row: rows x P bytes,
+ *             128  128 columns of 128 rows: ceil(rows / 128) x P bytes,
+ *           with P = 4 ceil(G / 4).
+ * Columns past cols have code 0, scale bytes past the G-th of a row are 0:
+ * every call that writes a matrix writes them so, and gc_fp8_matmul takes them so.
+ *
+ * Quantising a block (Q8 below): the scale is the least power of two, 2^-127 at
+ * least, that takes the block's largest magnitude to at most 448; a code is
+ * entry / scale rounded to the nearest E4M3 value (ties to the even code), with
+ * the entry's sign.  Nothing saturates.  A block with an entry that is not
+ * finite gets s = 255 and zero codes.  D8 gives back the values, exactly, in
+ * float32 (a value past its range, from bytes that no call here writes, is
+ * infinite). */
+
+/* Bytes of the two buffers; 0 when the shape is out of range (rows, cols >= 1
+ * and rows * 128 G <= 2^34; block_rows 1 or 128). */
+size_t gc_fp8_code_bytes(int64_t rows, int64_t cols);
+size_t gc_fp8_scale_bytes(int64_t rows, int64_t cols, int block_rows);
+
+/* Quantisation of a matrix x [rows x cols], rows ld entries apart (ld >= cols,
+ * (rows - 1) ld <= 2^40), float32 or bf16: the operands of gc_fp8_matmul.
+ *   codes, scales      Q8 along the rows: the 8-bit matrix rows x cols, or both NULL
+ *   codes_t, scales_t  Q8 along the columns, transposed: the 8-bit matrix
+ *                      cols x rows, or both NULL
+ * With both forms asked for, x is read once.  With block_rows 1 the two forms
+ * have blocks (and values) of their own; with block_rows 128 they have the same
+ * 128 x 128 blocks, so a weight has the same values in the forward product and
+ * in its input's gradient.  For y = x W^T the forward product takes x and W by
+ * rows; dx = dy W takes dy by rows and W by columns; dW = dy^T x takes dy and x
+ * by columns, in blocks of one row each.
+ * Errors: GC_ERR_ARG (null or misaligned pointer, no form asked for, half a
+ * form, shape, ld or block_rows out of range, overlapping buffers), GC_ERR_DTYPE,
+ * GC_ERR_HIP. */
+int gc_fp8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, int block_rows, uint8_t* codes,
+                    uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, void* stream);
+
+/* The values D8 of a held matrix: out has rows of cols entries, ldo entries
+ * apart (ldo >= cols, (rows - 1) ldo <= 2^40), float32 (exact) or bf16 (rounded
+ * once; exact unless below its least normal value).  Entries of out between the
+ * rows (cols .. ldo) are left alone.
+ * Errors: GC_ERR_ARG (null or misaligned pointer, shape, ldo or block_rows out
+ * of range, out overlapping the matrix), GC_ERR_DTYPE, GC_ERR_HIP. */
+int gc_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int block_rows, int64_t rows, int64_t cols, void* out,
+                      int64_t ldo, int out_dtype, void* stream);
+
+/* Workspace bytes of gc_fp8_matmul (0: none is needed, or a size is out of range). */
+size_t gc_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/* Product of two 8-bit matrices, both with the summed index along their rows:
+ *     out[i, j] = [out[i, j] +] sum_k D8(A)[i, k] * D8(B)[j, k]
+ * A is m x k in blocks of a_block_rows, B is n x k in blocks of b_block_rows;
+ * out has m rows of n entries, ldo entries apart (ldo >= n, (m - 1) ldo <= 2^40),
+ * float32 or bf16 (out_dtype), rounded once.  Entries of out between the rows
+ * (n .. ldo) are left alone.
+ *   float32  products are exact and summed in float32, in an order fixed by the
+ *            sizes; values below 2^-126 take part as the nearest multiple of
+ *            2^-133
+ *   bf16     products are added eight at a time, each cut off 13 binary places
+ *            below the leading bit of the largest of the eight, and those sums in
+ *            float32: at twice the rate, and off by about 1.4e-5 of the result's
+ *            size before the rounding to bf16, whose step is 2^-8
+ *   m, n     in [1, 2^30], k in [1, 2^24]; each matrix, and m x n, within the
+ *            range above
+ *   ws       >= gc_fp8_matmul_workspace_bytes(m, n, k) bytes (may be NULL for 0)
+ * out is what the compressors take as a gradient; accumulate != 0 adds up
+ * micro-batches.
+ * Errors: GC_ERR_ARG (null or misaligned pointer, size, ldo or block rows out of
+ * range, out or ws overlapping a buffer), GC_ERR_DTYPE, GC_ERR_WORKSPACE, GC_ERR_HIP. */
+int gc_fp8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int a_block_rows, const uint8_t* b_codes,
+                  const uint8_t* b_scales, int b_block_rows, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo,
+                  int out_dtype, int accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Accordion: per-layer norms and the l_low / l_high switch                 */

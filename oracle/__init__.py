@@ -25,7 +25,9 @@ P Q^T, residual into memory) are not spelled out on the pages; the oracle takes
 them in that plain order (see ``powersgd.py``).  The vectors of a gradient set
 (batch-norm parameters, biases) are sent uncompressed (``passthrough.py``).
 The 4-bit quantiser (``mxfp4.py``) follows the OCP Microscaling Formats
-specification; the pages name no quantising compressor.
+specification; the pages name no quantising compressor.  The 8-bit one
+(``fp8.py``) takes its element type from the OCP 8-bit floating point
+specification (E4M3) and its scale type from the former.
 
 Parity pins: every function here is checked in ``tests/test_oracle_*.py``
 against closed forms, brute force, library special cases or invariants fixed by
@@ -38,6 +40,7 @@ from .randk_ef import randk_ef_step
 from .powersgd import orthonormalize_mgs, powersgd_ef_step
 from .passthrough import passthrough_step
 from .mxfp4 import mxfp4_quantize, mxfp4_values, mxfp4_ef_step, mxfp4_decode, mxfp4_matmul
+from .fp8 import fp8_quantize, fp8_values, fp8_matmul
 from .norms import grad_norm
 from .accordion import accordion_select, LEVEL_LOW, LEVEL_HIGH
 from .memsgd import run_memsgd, QuadraticProblem
@@ -47,4 +50,5 @@ __all__ = [
     "magnitude_order", "randk_ef_step", "orthonormalize_mgs", "powersgd_ef_step", "passthrough_step", "grad_norm",
     "accordion_select", "LEVEL_LOW", "LEVEL_HIGH", "run_memsgd", "QuadraticProblem",
     "mxfp4_quantize", "mxfp4_values", "mxfp4_ef_step", "mxfp4_decode", "mxfp4_matmul",
+    "fp8_quantize", "fp8_values", "fp8_matmul",
 ]
