@@ -45,6 +45,11 @@ class gc_vec(C.Structure):
     _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("len", C.c_int64)]
 
 
+class gc_muon_mat(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("mem", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int32), ("m", C.c_int32),
+                ("scale", C.c_float)]
+
+
 def _sig(name, res, *args):
     f = getattr(lib, name)
     f.restype = res
@@ -88,6 +93,8 @@ _sig("gc_fp8_quantize", _i32, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp, 
 _sig("gc_fp8_dequantize", _i32, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _i32, _vp)
 _sig("gc_fp8_matmul_workspace_bytes", _sz, _i64, _i64, _i64)
 _sig("gc_fp8_matmul", _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i64, _i32, _i32, _vp, _sz, _vp)
+_sig("gc_muon_workspace_bytes", _sz, C.POINTER(gc_muon_mat), _i32)
+_sig("gc_muon_step", _i32, C.POINTER(gc_muon_mat), _i32, _i32, _i32, _f32, _i32, _i32, C.POINTER(C.c_float), _vp, _sz, _vp)
 _sig("gc_timing_enable", _i32, C.c_char_p)
 _sig("gc_timing_read", _i32, C.POINTER(C.c_double), C.POINTER(C.c_int64))
 _sig("gc_kernel_names", C.c_char_p)
@@ -102,7 +109,7 @@ EXPORTED = ["gc_status_str", "gc_last_error", "gc_topk_workspace_bytes", "gc_top
             "gc_mxfp4_code_bytes", "gc_mxfp4_scale_bytes", "gc_mxfp4_ef_encode", "gc_mxfp4_decode",
             "gc_mxfp4_quantize", "gc_mxfp4_matmul_workspace_bytes", "gc_mxfp4_matmul",
             "gc_fp8_code_bytes", "gc_fp8_scale_bytes", "gc_fp8_quantize", "gc_fp8_dequantize",
-            "gc_fp8_matmul_workspace_bytes", "gc_fp8_matmul",
+            "gc_fp8_matmul_workspace_bytes", "gc_fp8_matmul", "gc_muon_workspace_bytes", "gc_muon_step",
             "gc_timing_enable", "gc_timing_read", "gc_kernel_names"]
 
 
@@ -777,6 +784,77 @@ def gc_fp8_matmul(a_codes, a_scales, b_codes, b_scales, k: int, out, ws=None, a_
     _mx_call(dev, stream, "gc_fp8_matmul", lib.gc_fp8_matmul,
              (pac, pas, a_block_rows, pbc, pbs, b_block_rows, m, n, k, out.data_ptr(), ldo, _mx_dtype(out, "out"),
               1 if accumulate else 0, pw, wb))
+
+
+# ------------------------------------------------------------------ orthogonalised updates
+
+@dataclass
+class MuonMat:
+    """One matrix of gc_muon_step: grad (float32 or bf16), out (float32 or bf16) and the momentum mem (float32, or None),
+    all n x m; the update in out is `scale` times the orthogonalised one."""
+    grad: object
+    out: object
+    mem: object = None
+    scale: float = 1.0
+
+
+class MuonArray:
+    """The matrices of gc_muon_step marshalled once: checked and turned into the C array a single time, then passed to
+    every step on the same buffers (it keeps the tensors alive; they must stay in place)."""
+
+    def __init__(self, mats: Sequence[MuonMat]):
+        if _torch is None:
+            _mx_load()
+        self.mats = list(mats)
+        self.count = len(self.mats)
+        _need(self.count >= 1, "need at least one matrix")
+        first = self.mats[0]
+        self.dtype, self.out_dtype = _mx_dtype(first.grad, "grad"), _mx_dtype(first.out, "out")
+        self.dev = first.grad.get_device()
+        self.arr = (gc_muon_mat * self.count)()
+        for i, a in enumerate(self.mats):
+            _need(a.grad.dim() == 2 and a.grad.numel() > 0, f"mats[{i}].grad must be 2-D (n, m) with entries")
+            _need(a.grad.dtype == first.grad.dtype, "every gradient must have the first one's dtype")
+            _need(a.out.dtype == first.out.dtype, "every out must have the first one's dtype")
+            for t, name in ((a.grad, "grad"), (a.out, "out"), (a.mem, "mem")):
+                if t is None:
+                    continue
+                _need(t.shape == a.grad.shape, f"mats[{i}].{name} must have grad's shape")
+                _need(t.is_contiguous(), "expected a contiguous tensor")
+                if t.get_device() != self.dev:
+                    _mx_elsewhere(t)
+            if a.mem is not None:
+                _dtype_is(a.mem, _torch.float32, f"mats[{i}].mem")
+            n, m = a.grad.shape
+            _need(max(n, m) <= 1 << 22, "n and m must be at most 2^22")       # the C struct's are ints
+            self.arr[i] = gc_muon_mat(a.grad.data_ptr(), None if a.mem is None else a.mem.data_ptr(), a.out.data_ptr(),
+                                      n, m, float(a.scale))
+
+
+def gc_muon_workspace_bytes(mats) -> int:
+    """mats: a list of MuonMat, or a MuonArray built from one."""
+    a = mats if isinstance(mats, MuonArray) else MuonArray(mats)
+    return int(lib.gc_muon_workspace_bytes(a.arr, a.count))
+
+
+def gc_muon_step(mats, beta: float, ws, nesterov: bool = True, steps: int = 5, coefs=None, stream=None) -> None:
+    """Momentum, then `steps` Newton-Schulz steps: out = scale * (the update with its singular values driven to about one).
+    mats: a list of MuonMat, or a MuonArray built from one.  coefs: None, one (a, b, c), or one for each step."""
+    a = mats if isinstance(mats, MuonArray) else MuonArray(mats)
+    steps = int(steps)
+    pc = None
+    if coefs is not None:
+        c = np.ascontiguousarray(coefs, np.float32)
+        _need(c.shape in ((3,), (steps, 3)), "coefs must be (a, b, c), or one of them for each step")
+        _need(1 <= steps <= 32, "steps must be in [1, 32]")
+        c = np.ascontiguousarray(np.broadcast_to(c, (steps, 3)))
+        pc = c.ctypes.data_as(C.POINTER(C.c_float))
+    if ws.get_device() != a.dev:
+        _mx_elsewhere(ws)
+    if not ws.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    _mx_call(a.dev, stream, "gc_muon_step", lib.gc_muon_step,
+             (a.arr, a.count, a.dtype, a.out_dtype, float(beta), 1 if nesterov else 0, steps, pc, ws.data_ptr(), ws.nbytes))
 
 
 # ------------------------------------------------------------------ timing hooks

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgc.so")
 SOURCES = ["common.hip", "topk.hip", "powersgd.hip", "norm.hip", "passthrough.hip", "noalloc.hip",
-           "mxfp4.hip", "mxfp4_matmul.hip", "fp8.hip", "fp8_matmul.hip"]
+           "mxfp4.hip", "mxfp4_matmul.hip", "fp8.hip", "fp8_matmul.hip", "muon.hip"]
 ARCH = os.environ.get("GC_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"

@@ -14,7 +14,8 @@
  *   - MXFP4 (microscaled 4-bit floating point): the compressor with memory, the
  *     decode of gathered messages, the quantisation and the product of matrices,
  *   - 8-bit floating point with a scale for each block of 128: the quantisation
- *     and the product of matrices.
+ *     and the product of matrices,
+ *   - momentum and orthogonalisation of updates by Newton-Schulz products.
  *
  * Conventions shared by every entry point
  *   - Tensor pointers are DEVICE pointers owned by the caller unless marked
@@ -32,8 +33,8 @@
  *     gc_last_error() gives a message for the last failure on this thread.
  *   - Gradients may be float32 (GC_F32) or bfloat16 (GC_BF16); memory, factors
  *     and decoded outputs are always float32, except that gc_mxfp4_decode,
- *     gc_mxfp4_matmul, gc_fp8_dequantize and gc_fp8_matmul write either type
- *     (out_dtype).
+ *     gc_mxfp4_matmul, gc_fp8_dequantize, gc_fp8_matmul and gc_muon_step write
+ *     either type (out_dtype).
  *   - Results are deterministic: the same inputs give the same bits on every
  *     call (all reductions have a fixed order; no floating-point atomics).
  *   - Calls that share a workspace must not overlap in time (use one stream).
@@ -486,13 +487,61 @@ size_t gc_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
  *   m, n     in [1, 2^30], k in [1, 2^24]; each matrix, and m x n, within the
  *            range above
  *   ws       >= gc_fp8_matmul_workspace_bytes(m, n, k) bytes (may be NULL for 0)
- * out is what the compressors take as a gradient; accumulate != 0 adds up
- * micro-batches.
+ * out is what the compressors and gc_muon_step take as a gradient; accumulate
+ * != 0 adds up micro-batches.
  * Errors: GC_ERR_ARG (null or misaligned pointer, size, ldo or block rows out of
  * range, out or ws overlapping a buffer), GC_ERR_DTYPE, GC_ERR_WORKSPACE, GC_ERR_HIP. */
 int gc_fp8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int a_block_rows, const uint8_t* b_codes,
                   const uint8_t* b_scales, int b_block_rows, int64_t m, int64_t n, int64_t k, void* out, int64_t ldo,
                   int out_dtype, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Orthogonalised updates                                                    */
+/* ------------------------------------------------------------------------ */
+
+/* One matrix of gc_muon_step, n x m, row-major (a conv weight reshaped to
+ * out x (in*kh*kw)). */
+typedef struct gc_muon_mat {
+    const void* grad;  /* [n*m] float32 or bf16, read only                          */
+    float* mem;        /* [n*m] in/out: momentum (NULL: none, u = grad)             */
+    void* out;         /* [n*m] out: the update, float32 or bf16                    */
+    int32_t n, m;      /* 1 <= n, m <= 2^22; n*m <= INT32_MAX                       */
+    float scale;       /* factor of the update                                      */
+} gc_muon_mat;
+
+/* Workspace bytes for gc_muon_step on these matrices ([host] array; the shapes
+ * alone are read).  Returns 0 when an entry is out of range. */
+size_t gc_muon_workspace_bytes(const gc_muon_mat* mats, int nmats);
+
+/* One step of momentum and orthogonalisation by Newton-Schulz products (as in the
+ * Muon optimiser) on every matrix of mats ([host], nmats >= 1):
+ *     mem = fl32(fl32(beta * mem) + grad)
+ *     u   = fl32(grad + fl32(beta * mem)) if nesterov != 0, else mem;  grad without a mem
+ *     X   = u / |u|_F
+ *     steps times:  A = X X^T;  X = a X + (b A + c A A) X
+ *     out = scale * X
+ * (from the other side, X^T X, for n > m: the same polynomial).  Where PowerSGD's
+ * orthonormalisation makes a few columns orthonormal, this drives every singular
+ * value of the update to about one and keeps its singular vectors.  A matrix of
+ * zeros gives zeros, one whose u has an entry that is not finite NaN everywhere.
+ *   grad_dtype, out_dtype   GC_F32 or GC_BF16, for all matrices
+ *   steps    1 to 32 (5 is usual)
+ *   coefs    [host] 3 * steps floats, a, b, c of each step, or NULL: 3.4445,
+ *            -4.7750, 2.0315 at every step.  Singular values, which start in
+ *            [0, 1], may not pass 4, nor may |a + b s^2 + c s^4| pass 16.
+ *   ws       >= gc_muon_workspace_bytes(mats, nmats) bytes
+ * Sums are in float32 (the norm's in float64); X, A and a + b A + c A A are held as
+ * pairs of 11-bit floating point numbers, 22 to 24 bits together and nothing below
+ * 2^-37 (X's entries are at most 4), and rounded once to out.  The usual coefficients make what a step rounds up to 3.4 times
+ * as large with every step that follows: a float32 out is within about 2e-4 of
+ * the exact one (2-norm over the matrix's), and within 2e-6 to 2e-5 for matrices
+ * whose singular values are not far apart.
+ * Kernel launches only: no copy, no allocation, no synchronisation, so the call may
+ * be captured in a HIP graph.  [host] arrays may be reused as soon as it returns.
+ * Errors: GC_ERR_ARG (null or misaligned pointer, shape, steps or coefs out of
+ * range, a written buffer overlapping another), GC_ERR_DTYPE, GC_ERR_WORKSPACE, GC_ERR_HIP. */
+int gc_muon_step(const gc_muon_mat* mats, int nmats, int grad_dtype, int out_dtype, float beta, int nesterov, int steps,
+                 const float* coefs, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Accordion: per-layer norms and the l_low / l_high switch                 */

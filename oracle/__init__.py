@@ -27,7 +27,8 @@ them in that plain order (see ``powersgd.py``).  The vectors of a gradient set
 The 4-bit quantiser (``mxfp4.py``) follows the OCP Microscaling Formats
 specification; the pages name no quantising compressor.  The 8-bit one
 (``fp8.py``) takes its element type from the OCP 8-bit floating point
-specification (E4M3) and its scale type from the former.
+specification (E4M3) and its scale type from the former.  ``muon.py`` follows
+the Muon optimiser's description.
 
 Parity pins: every function here is checked in ``tests/test_oracle_*.py``
 against closed forms, brute force, library special cases or invariants fixed by
@@ -41,6 +42,7 @@ from .powersgd import orthonormalize_mgs, powersgd_ef_step
 from .passthrough import passthrough_step
 from .mxfp4 import mxfp4_quantize, mxfp4_values, mxfp4_ef_step, mxfp4_decode, mxfp4_matmul
 from .fp8 import fp8_quantize, fp8_values, fp8_matmul
+from .muon import muon_step, newton_schulz
 from .norms import grad_norm
 from .accordion import accordion_select, LEVEL_LOW, LEVEL_HIGH
 from .memsgd import run_memsgd, QuadraticProblem
@@ -50,5 +52,5 @@ __all__ = [
     "magnitude_order", "randk_ef_step", "orthonormalize_mgs", "powersgd_ef_step", "passthrough_step", "grad_norm",
     "accordion_select", "LEVEL_LOW", "LEVEL_HIGH", "run_memsgd", "QuadraticProblem",
     "mxfp4_quantize", "mxfp4_values", "mxfp4_ef_step", "mxfp4_decode", "mxfp4_matmul",
-    "fp8_quantize", "fp8_values", "fp8_matmul",
+    "fp8_quantize", "fp8_values", "fp8_matmul", "muon_step", "newton_schulz",
 ]
