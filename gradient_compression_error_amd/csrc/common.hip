@@ -124,7 +124,7 @@ const char* gc_kernel_names(void) {
            "norm_partial,norm_final,passthrough,"
            "mxfp4_ef,mxfp4_rows,mxfp4_cols,mxfp4_decode,mxfp4_wave,mxfp4_tile,mxfp4_join,"
            "fp8_rows,fp8_tiles,fp8_values,fp8_wave,fp8_tile,fp8_join,"
-           "muon_moment,muon_start,muon_product,muon_join";
+           "muon_moment,muon_start,muon_tile,muon_join";
 }
 
 }  // extern "C"

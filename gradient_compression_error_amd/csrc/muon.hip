@@ -12,7 +12,10 @@
 // operands alone are 0.003 to 0.15 off in the end.  So X, A and P are held as pairs of f16,
 // hi = fl16(v 2^e), lo = fl16(v 2^e - hi), 22 to 24 bits together, and a product is three
 // matrix instructions, hi hi + hi lo + lo hi, summed in float32: as good as float32
-// products.  The powers of two (SX, SA, SP) keep hi below f16's largest value, which the
+// products.  The last step's roundings are not enlarged: where the result is rounded to bf16
+// anyway, its A and its P X take the hi parts alone (ONE), which is 0.0002 to 0.0008 off, a
+// twentieth to a half of the rounding to bf16 (A A does not: the diagonal of A has entries
+// alike, whose roundings add up to 0.002).  The powers of two (SX, SA, SP) keep hi below f16's largest value, which the
 // caller's coefficients are checked for, and lo above its least for all but entries that
 // do not matter; f16 subnormals are kept by the matrix instructions.
 //
@@ -32,7 +35,7 @@ namespace gc {
 namespace {
 
 constexpr int MU_MAX = 64;             // matrices of a launch
-constexpr int MU_TILE = 16384;         // entries of a partial sum of squares
+constexpr int MU_SUMS = 512;           // partial sums of squares of a matrix, at most
 constexpr int64_t MU_MAX_SIDE = int64_t(1) << 22;
 constexpr int MU_MAX_STEPS = 32;
 constexpr int MU_MAX_PARTS = 64;
@@ -47,7 +50,7 @@ struct Shape {
     long long base;
     int n, m;
 };
-__host__ __device__ inline long long mu_groups(long long cols) { return (cols + 31) / 32; }
+__host__ __device__ inline int64_t mu_groups(int64_t cols) { return (cols + 31) / 32; }
 __host__ __device__ inline long long at_x(const Shape& s) { return s.base; }
 __host__ __device__ inline long long at_xt(const Shape& s, int which) {
     return at_x(s) + s.n * mu_groups(s.m) * 128 + which * (s.m * mu_groups(s.n) * 128);
@@ -55,6 +58,14 @@ __host__ __device__ inline long long at_xt(const Shape& s, int which) {
 __host__ __device__ inline long long at_a(const Shape& s) { return at_xt(s, 2); }
 __host__ __device__ inline long long at_p(const Shape& s) { return at_a(s) + s.n * mu_groups(s.n) * 128; }
 __host__ __device__ inline long long at_parts(const Shape& s) { return at_p(s) + s.n * mu_groups(s.n) * 128; }
+
+// Entries of a partial sum of squares: a multiple of 1024, so that few sums are left to add
+// for a large matrix and a small one still has several workgroups.
+__host__ __device__ inline int mu_chunk(long long entries) {
+    const long long even = (entries + MU_SUMS - 1) / MU_SUMS;
+    return static_cast<int>(even <= 2048 ? 2048 : (even + 1023) / 1024 * 1024);
+}
+__host__ __device__ inline int mu_sums(long long entries) { return static_cast<int>((entries + mu_chunk(entries) - 1) / mu_chunk(entries)); }
 
 // One launch's work: workgroups begin[i] .. are matrix i's.
 struct Batch {
@@ -78,12 +89,17 @@ struct Sources {
     int count;
 };
 
+// Eight values as pairs: two conversions and a mixed subtraction for two of them.
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ f16x8 halves(const float (&v)[8], f16x8& lo) {
     f16x8 hi;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        hi[q] = static_cast<_Float16>(v[q]);
-        lo[q] = static_cast<_Float16>(v[q] - static_cast<float>(hi[q]));
+    for (int q = 0; q < 8; q += 2) {
+        const f16x2 h = __builtin_convertvector((f32x2{v[q], v[q + 1]}), f16x2);
+        const f16x2 l = __builtin_convertvector((f32x2{__builtin_fmaf(static_cast<float>(h[0]), -1.0f, v[q]),
+                                                       __builtin_fmaf(static_cast<float>(h[1]), -1.0f, v[q + 1])}), f16x2);
+        hi[q] = h[0]; hi[q + 1] = h[1];
+        lo[q] = l[0]; lo[q + 1] = l[1];
     }
     return hi;
 }
@@ -91,9 +107,11 @@ __device__ __forceinline__ f16x8 halves(const float (&v)[8], f16x8& lo) {
 // Writes eight columns of a held row, `col` a multiple of 8; columns from `cols` on are zeros.
 __device__ __forceinline__ void put8(char* row, int col, int cols, float (&v)[8]) {
     if (col >= ((cols + 31) & ~31)) return;
+    if (col + 8 > cols) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        if (col + q >= cols) v[q] = 0.0f;
+        for (int q = 0; q < 8; ++q)
+            if (col + q >= cols) v[q] = 0.0f;
+    }
     f16x8 lo;
     const f16x8 hi = halves(v, lo);
     char* const to = row + (col >> 5) * 128ll + (col & 31) * 2;
@@ -108,16 +126,17 @@ __device__ __forceinline__ float direction(float mem, float beta, float g, bool 
     return nesterov ? __fadd_rn(g, __fmul_rn(beta, mem)) : mem;
 }
 
-// mem = beta mem + grad, and the sum of u^2 over MU_TILE entries in float64.
+// mem = beta mem + grad, and the sum of u^2 over a chunk of the entries in float64.
 template <bool BF16>
 __global__ __launch_bounds__(256) void muon_moment(const Sources src, float beta, int nesterov, double* partial) {
     __shared__ double sums[4];
-    const int w = find_segment(src.begin, src.count, blockIdx.x), tile = blockIdx.x - src.begin[w];
+    const int w = find_segment(src.begin, src.count, blockIdx.x), chunk = blockIdx.x - src.begin[w];
     const void* const grad = src.grad[w];
     float* const mem = src.mem[w];
-    const long long count = static_cast<long long>(src.n[w]) * src.m[w], first = static_cast<long long>(tile) * MU_TILE;
-    const long long quads = min(count, first + MU_TILE) / 4;
+    const long long count = static_cast<long long>(src.n[w]) * src.m[w], size = mu_chunk(count), first = chunk * size;
+    const long long quads = min(count, first + size) / 4;
     double sum = 0.0;
+#pragma unroll 4
     for (long long q = first / 4 + threadIdx.x; q < quads; q += 256) {
         const float4 g = load_grad4<BF16>(grad, q);
         float4 u = g;
@@ -132,7 +151,7 @@ __global__ __launch_bounds__(256) void muon_moment(const Sources src, float beta
                (static_cast<double>(u.z) * u.z + static_cast<double>(u.w) * u.w);
     }
     const long long i = quads * 4 + threadIdx.x;             // up to three entries behind the last four
-    if (quads * 4 < first + MU_TILE && i < count) {
+    if (quads * 4 < first + size && i < count) {
         const float g = load_grad1<BF16>(grad, i);
         float u = g;
         if (mem) {
@@ -145,7 +164,7 @@ __global__ __launch_bounds__(256) void muon_moment(const Sources src, float beta
     sum = wave_sum(sum);
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) partial[src.partial[w] + tile] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    if (threadIdx.x == 0) partial[src.partial[w] + chunk] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 // X = u / |u| by rows and transposed, 64 x 64 entries a workgroup.  A matrix of zeros
@@ -159,7 +178,17 @@ __global__ __launch_bounds__(256) void muon_start(const Sources src, float beta,
     const int i0 = t / across * 64, j0 = t % across * 64;
     const void* const grad = src.grad[w];
     const float* const mem = src.mem[w];
-    const int parts = static_cast<int>((static_cast<long long>(n) * m + MU_TILE - 1) / MU_TILE);
+    float u[16];                                             // fetched while the norm is
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+        const int i = i0 + p * 4 + (threadIdx.x >> 6), j = j0 + (threadIdx.x & 63);
+        const bool in = i < n && j < m;
+        const long long at = in ? static_cast<long long>(i) * m + j : 0;
+        u[p] = load_grad1<BF16>(grad, at);
+        if (mem) u[p] = direction(mem[at], beta, u[p], nesterov);
+        if (!in) u[p] = 0.0f;
+    }
+    const int parts = mu_sums(static_cast<long long>(n) * m);
     double sum = 0.0;
     for (int p = threadIdx.x; p < parts; p += 256) sum += partial[src.partial[w] + p];
     sum = wave_sum(sum);
@@ -167,16 +196,10 @@ __global__ __launch_bounds__(256) void muon_start(const Sources src, float beta,
     __syncthreads();
     const double norm = sqrt((sums[0] + sums[1]) + (sums[2] + sums[3]));
     const double by = norm == 0.0 ? 0.0 : (norm < INFINITY ? SX / norm : static_cast<double>(NAN));
-#pragma unroll 4
+#pragma unroll
     for (int p = 0; p < 16; ++p) {
-        const int i = p * 4 + (threadIdx.x >> 6), j = threadIdx.x & 63;
-        float x = 0.0f;
-        if (i0 + i < n && j0 + j < m) {
-            const long long at = static_cast<long long>(i0 + i) * m + j0 + j;
-            const float g = load_grad1<BF16>(grad, at);
-            x = static_cast<float>((mem ? direction(mem[at], beta, g, nesterov) : g) * by);
-        }
-        tile[i][j] = x;
+        const bool in = i0 + p * 4 + (threadIdx.x >> 6) < n && j0 + (threadIdx.x & 63) < m;
+        tile[p * 4 + (threadIdx.x >> 6)][threadIdx.x & 63] = in ? static_cast<float>(u[p] * by) : 0.0f;   // (by may be NaN)
     }
     __syncthreads();
     const bool turned = n > m;
@@ -202,7 +225,8 @@ __global__ __launch_bounds__(256) void muon_start(const Sources src, float beta,
 
 // ---------------------------------------------------------------- products
 
-enum { GRAM, GRAM_PART, POLY, APPLY, LAST_F32, LAST_BF16 };
+enum { GRAM, POLY, APPLY, LAST_F32, LAST_BF16 };
+constexpr bool symmetric(int kind) { return kind == GRAM || kind == POLY; }
 
 // The I-th row and J-th column of the t-th tile on or below the diagonal.
 __device__ __forceinline__ void below_diagonal(int t, int& I, int& J) {
@@ -213,54 +237,193 @@ __device__ __forceinline__ void below_diagonal(int t, int& I, int& J) {
     J = t - i * (i + 1) / 2;
 }
 
-// A tile BM x BN of L R^T for held matrices L and R, the groups of k in LDS in a ring of
-// RING, copied straight from memory; waves WM x WN.  A group is worked off in two stages of 16
-// columns, and a wave reads the fragments of the next stage while its matrix instructions
-// work on the present one.  LDS holds a row's 128 bytes together, its eight pieces permuted
-// so that a fragment's reads meet no bank twice: piece b of row i of a fragment at slot
-// b ^ (i >> 1 & 7).
-template <int BM, int BN, int WM, int WN, int RING, int KIND>
-__global__ __launch_bounds__(WM* WN * 64) void muon_product(const Batch batch, const Ends ends, char* ws, int turn, float ca, float cb,
-                                                          float cc) {
+// One workgroup's product: a tile of L R^T at (i0, j0), over `groups` groups of k.
+struct Job {
+    Shape s;
+    int w, i0, j0, groups;
+    int part;                                                // of k, or -1: all of it
+    bool diagonal;
+    const unsigned char *left, *right;                       // the tile's first rows, at its first group
+    int rows_l, rows_r;                                      // rows from there on
+    unsigned pitch;
+};
+template <int KIND, int BM, int BN>
+__device__ __forceinline__ Job job_of(const Batch& batch, char* ws, int turn) {
+    Job b;
+    const int block = static_cast<int>(xcd_place(blockIdx.x, gridDim.x));
+    b.w = find_segment(batch.begin, batch.count, block);
+    b.s = batch.s[b.w];
+    const int t = block - batch.begin[b.w];
+    int I, J, first = 0;
+    b.part = -1;
+    b.groups = static_cast<int>(mu_groups(KIND == GRAM ? b.s.m : b.s.n));
+    b.pitch = static_cast<unsigned>(b.groups) * 128;
+    if constexpr (symmetric(KIND)) {
+        int tile = t;
+        if (KIND == GRAM && batch.per[b.w] < b.groups) {     // in parts
+            const int side = (b.s.n + BM - 1) / BM, tiles = side * (side + 1) / 2;
+            b.part = t / tiles;
+            tile = t - b.part * tiles;
+            first = b.part * batch.per[b.w];
+            b.groups = min(batch.per[b.w], b.groups - first);
+        }
+        below_diagonal(tile, I, J);
+    } else {
+        // bands of four tile rows, so that neighbours share operands
+        const int tiles_m = (b.s.n + BM - 1) / BM, tiles_n = (b.s.m + BN - 1) / BN;
+        const int band = t / (4 * tiles_n), height = min(4, tiles_m - band * 4), in = t - band * 4 * tiles_n;
+        I = band * 4 + in % height;
+        J = in / height;
+    }
+    I = __builtin_amdgcn_readfirstlane(I);
+    J = __builtin_amdgcn_readfirstlane(J);
+    b.i0 = I * BM;
+    b.j0 = J * BN;
+    b.diagonal = I == J;
+    const char* const left = ws + (KIND == GRAM ? at_x(b.s) : KIND == POLY ? at_a(b.s) : at_p(b.s));
+    const char* const right = symmetric(KIND) ? left : ws + at_xt(b.s, turn);
+    b.left = reinterpret_cast<const unsigned char*>(left) + static_cast<long long>(b.i0) * b.pitch + first * 128ll;
+    b.right = reinterpret_cast<const unsigned char*>(right) + static_cast<long long>(b.j0) * b.pitch + first * 128ll;
+    b.rows_l = b.s.n - b.i0;
+    b.rows_r = (symmetric(KIND) ? b.s.n : b.s.m) - b.j0;
+    return b;
+}
+
+// The sums of 32 rows x COLS columns at (row0, col0), in LDS, to where they go: one wave's
+// work.  Element (r, c) lies in the float4 (c / 4) ^ (r % 8) of row r.  They leave by rows, eight
+// columns a lane, and (for X, and for A and P off the diagonal) transposed, eight rows of a
+// column a lane, 32 rows one group.
+template <int KIND, int COLS>
+__device__ __forceinline__ void emit(float* region, const Job& b, int row0, int col0, const Ends& ends, char* ws, int turn, float ca,
+                                     float cb, float cc) {
+    constexpr bool LAST = KIND == LAST_F32 || KIND == LAST_BF16, BF16 = KIND == LAST_BF16;
+    const Shape& s = b.s;
+    const int lane = threadIdx.x & 63, rows = s.n, cols = symmetric(KIND) ? s.n : s.m;
+    if (row0 >= rows || col0 >= cols) return;
+    const float by = KIND == GRAM ? (b.part < 0 ? SA / (SX * SX) : 1.0f) : KIND == APPLY ? 1.0f / SP : LAST ? ends.scale[b.w] / (SP * SX) : 1.0f;
+    const bool turned = LAST && ends.turned[b.w];
+    if (!turned) {
+        constexpr int PER_ROW = COLS / 8;
+        f16x8 old[KIND == POLY ? COLS / 16 : 1][2];          // of A, fetched together
+        if constexpr (KIND == POLY) {
+#pragma unroll
+            for (int p = 0; p < COLS / 16; ++p) {
+                const int row = min(row0 + (p * 64 + lane) / PER_ROW, rows - 1), col = min(col0 + (p * 64 + lane) % PER_ROW * 8, (cols - 1) & ~7);
+                const char* const from = ws + at_a(s) + row * mu_groups(s.n) * 128 + (col >> 5) * 128ll + (col & 31) * 2;
+                old[p][0] = *reinterpret_cast<const f16x8*>(from);
+                old[p][1] = *reinterpret_cast<const f16x8*>(from + 64);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < COLS / 16; ++p) {
+            const int r = (p * 64 + lane) / PER_ROW, c = (p * 64 + lane) % PER_ROW * 8, row = row0 + r, col = col0 + c;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float4 f = *reinterpret_cast<const float4*>(region + r * COLS + ((c / 4 + q) ^ (r & 7)) * 4);
+                v[4 * q] = by * f.x; v[4 * q + 1] = by * f.y; v[4 * q + 2] = by * f.z; v[4 * q + 3] = by * f.w;
+            }
+            if (row >= rows) continue;
+            if (KIND == GRAM && b.part >= 0) {
+                const long long ld = mu_groups(s.n) * 32;
+                if (col < ld) {
+                    float4* const to = reinterpret_cast<float4*>(ws + at_parts(s) + ((static_cast<long long>(b.part) * s.n + row) * ld + col) * 4);
+                    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+                continue;
+            }
+            if constexpr (LAST) {
+                const long long at = static_cast<long long>(row) * s.m + col;
+                if (col + 8 <= s.m) {
+                    store_out<BF16>(ends.out[b.w], at, v);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (col + q < s.m) store1<BF16>(ends.out[b.w], at + q, v[q]);
+                }
+            } else {
+                if constexpr (KIND == POLY) {                // c A^2 + b A + a I, all times SP
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        v[q] = cc * (SP / (SA * SA)) * v[q] + cb * (SP / SA) * (static_cast<float>(old[p][0][q]) + static_cast<float>(old[p][1][q]));
+                        if (row == col + q) v[q] += ca * SP;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)              // for the transposed form
+                        *reinterpret_cast<float4*>(region + r * COLS + ((c / 4 + q) ^ (r & 7)) * 4) =
+                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                }
+                put8(ws + (KIND == GRAM ? at_a(s) : KIND == POLY ? at_p(s) : at_x(s)) + row * mu_groups(cols) * 128, col, cols, v);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    if constexpr (LAST) {
+        if (!turned) return;
+#pragma unroll
+        for (int p = 0; p < COLS / 16; ++p) {                // eight rows of a column a lane
+            const int c = p * 16 + (lane >> 2), k = (lane & 3) * 8, col = col0 + c;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = by * region[(k + q) * COLS + ((c >> 2) ^ (k + q & 7)) * 4 + (c & 3)];
+            if (col >= cols) continue;
+            const long long at = static_cast<long long>(col) * s.n + row0 + k;
+            if (row0 + k + 8 <= s.n) {
+                store_out<BF16>(ends.out[b.w], at, v);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (row0 + k + q < s.n) store1<BF16>(ends.out[b.w], at + q, v[q]);
+            }
+        }
+    } else {
+        if (symmetric(KIND) && (b.diagonal || b.part >= 0)) return;   // (a diagonal tile is its own mirror image)
+        char* const to = ws + (KIND == GRAM ? at_a(s) : KIND == POLY ? at_p(s) : at_xt(s, 1 - turn));
+        const long long pitch = mu_groups(s.n) * 128;
+        const float factor = KIND == POLY ? 1.0f : by;
+#pragma unroll
+        for (int p = 0; p < COLS / 16; ++p) {                // eight rows of a column a lane
+            const int c = p * 16 + (lane >> 2), k = (lane & 3) * 8, col = col0 + c;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = factor * region[(k + q) * COLS + ((c >> 2) ^ (k + q & 7)) * 4 + (c & 3)];
+            if (col < cols) put8(to + col * pitch, row0 + k, s.n, v);
+        }
+    }
+}
+
+// A 32 x 32 fragment of sums (column lane % 32 of the second factor's, so row lane % 32) to LDS.
+template <int COLS>
+__device__ __forceinline__ void lay(float* region, int y, const f32x16& acc) {
+    const int lane = threadIdx.x & 63, i = lane & 31;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(region + i * COLS + ((8 * y + 2 * r + (lane >> 5)) ^ (i & 7)) * 4) =
+            make_float4(acc[4 * r], acc[4 * r + 1], acc[4 * r + 2], acc[4 * r + 3]);
+}
+
+// A tile BM x BN, the groups of k in LDS in a ring of RING, copied straight from memory;
+// waves WM x WN.  A group is worked off in two stages of 16 columns (one of 32, for the
+// smallest tile), and a wave reads the fragments of the next stage while its matrix
+// instructions work on the present one.  LDS
+// holds a row's 128 bytes together, its eight pieces permuted so that a fragment's reads
+// meet no bank twice: piece b of row i of a fragment at slot b ^ (i >> 1 & 7).
+template <int BM, int BN, int WM, int WN, int RING, int KIND, bool ONE>
+__global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Batch batch, const Ends ends, char* ws, int turn, float ca, float cb,
+                                                       float cc) {
     constexpr int NW = WM * WN, ROWS = BM + BN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr int CP = ROWS / 8 / NW;                       // 8-row copies a wave makes for a group
     constexpr int GROUP = ROWS * 128;
-    constexpr bool SYMMETRIC = KIND == GRAM || KIND == GRAM_PART || KIND == POLY;
-    static_assert(CP * 8 * NW == ROWS && BM % (8 * NW) == 0 && NW % 4 == 0 && RING % 2 == 0 && (!SYMMETRIC || BM == BN), "tile and waves must fit");
+    constexpr int S = MI * NI == 1 ? 2 : 1;                 // steps of 16 columns of a stage: enough work to cover LDS's latency
+    static_assert(CP * 8 * NW == ROWS && BM % (8 * NW) == 0 && NW % 4 == 0 && (!symmetric(KIND) || BM == BN), "tile and waves must fit");
     __shared__ __attribute__((aligned(1024))) unsigned char lds[RING * GROUP];
     const unsigned lds_at = static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)lds));
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, i = lane & 31, wm = wave / WN, wn = wave % WN;
-
-    const int block = static_cast<int>(xcd_place(blockIdx.x, gridDim.x));
-    const int w = find_segment(batch.begin, batch.count, block);
-    const Shape s = batch.s[w];
-    int t = block - batch.begin[w], I, J, first = 0, groups, part = 0;
-    if constexpr (SYMMETRIC) {
-        const int side = (s.n + BM - 1) / BM, tiles = side * (side + 1) / 2;
-        part = t / tiles;
-        below_diagonal(t % tiles, I, J);
-        groups = static_cast<int>(mu_groups(KIND == POLY ? s.n : s.m));
-        if constexpr (KIND != POLY) {
-            first = part * batch.per[w];
-            groups = min(batch.per[w], groups - first);
-        }
-    } else {
-        const int tiles_m = (s.n + BM - 1) / BM, tiles_n = (s.m + BN - 1) / BN;
-        const int band = t / (4 * tiles_n), height = min(4, tiles_m - band * 4), in = t - band * 4 * tiles_n;
-        I = band * 4 + in % height;
-        J = in / height;
-        groups = static_cast<int>(mu_groups(s.n));
-    }
-    I = __builtin_amdgcn_readfirstlane(I);
-    J = __builtin_amdgcn_readfirstlane(J);
-    const int i0 = I * BM, j0 = J * BN;
-    const int rows_l = s.n, rows_r = SYMMETRIC ? s.n : s.m;
-    const unsigned pitch = static_cast<unsigned>(mu_groups(KIND == GRAM || KIND == GRAM_PART ? s.m : s.n)) * 128;
-    const char* const left = ws + (KIND == GRAM || KIND == GRAM_PART ? at_x(s) : KIND == POLY ? at_a(s) : at_p(s));
-    const char* const right = SYMMETRIC ? left : ws + at_xt(s, turn);
-    const unsigned char* const base_l = reinterpret_cast<const unsigned char*>(left) + static_cast<long long>(i0) * pitch + first * 128ll;
-    const unsigned char* const base_r = reinterpret_cast<const unsigned char*>(right) + static_cast<long long>(j0) * pitch + first * 128ll;
+    const Job b = job_of<KIND, BM, BN>(batch, ws, turn);
+    // a unit is what a place of the ring holds of a row: a group, or the hi halves of two
+    const int groups = b.groups, units = ONE ? (groups + 1) / 2 : groups;
 
     // Where this wave's copies come from: rows past the end are the last one again (their
     // results are not written); 256 rows of 2^24 bytes stay within 32 bits.
@@ -269,34 +432,46 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_product(const Batch batch, c
 #pragma unroll
     for (int c = 0; c < CP; ++c) {
         const int r = (c * NW + wave) * 8 + (lane >> 3);
-        off[c] = static_cast<unsigned>(c * 8 * NW < BM ? min(r, rows_l - 1 - i0) : min(r - BM, rows_r - 1 - j0)) * pitch + piece * 16;
+        off[c] = static_cast<unsigned>(c * 8 * NW < BM ? min(r, b.rows_l - 1) : min(r - BM, b.rows_r - 1)) * b.pitch + piece * 16 +
+                 (ONE && piece >= 4 ? 64 : 0);
     }
-    auto copy = [&](int c, int group, int place) {
-        copy16((c * 8 * NW < BM ? base_l : base_r) + min(group, groups - 1) * 128ll, off[c], lds_at + place * GROUP + (c * NW + wave) * 1024);
+    const unsigned second = ONE && piece >= 4 ? 128 : 0;     // what leads from the second group back to the first
+    auto copy = [&](int c, int unit, int place) {            // units past the end are the last again, a group past it the one before
+        const int u = min(unit, units - 1);
+        const unsigned back = ONE && 2 * u + 1 == groups ? second : 0;
+        copy16((c * 8 * NW < BM ? b.left : b.right) + u * (ONE ? 256ll : 128ll), off[c] - back, lds_at + place * GROUP + (c * NW + wave) * 1024);
     };
 
     const int l_at = wm * MI * 4096 + i * 128, r_at = BM * 128 + wn * NI * 4096 + i * 128;
-    int c_at[2][2];                                          // byte of a row, by stage, hi and lo
+    int c_at[2][2];                                          // byte of a row, by stage, hi and lo (or group)
 #pragma unroll
     for (int q = 0; q < 4; ++q) c_at[q >> 1][q & 1] = (((q & 1) * 4 + 2 * (q >> 1) + half) ^ ((i >> 1) & 7)) * 16;
     auto read = [&](auto& l, auto& r, int place, int stage) {
 #pragma unroll
-        for (int y = 0; y < NI; ++y)
+        for (int k = 0; k < S; ++k) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) r[y][h] = *reinterpret_cast<const f16x8*>(lds + place * GROUP + r_at + y * 4096 + c_at[stage][h]);
+            for (int y = 0; y < NI; ++y)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) r[k][y][h] = *reinterpret_cast<const f16x8*>(lds + place * GROUP + r_at + y * 4096 + c_at[stage * S + k][h]);
+#pragma unroll
+            for (int x = 0; x < MI; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) l[k][x][h] = *reinterpret_cast<const f16x8*>(lds + place * GROUP + l_at + x * 4096 + c_at[stage * S + k][h]);
+        }
+    };
+
+    // A matrix instruction waits for the one before on the same sums: with few fragments the
+    // products hi hi, hi lo and lo hi have sums of their own.
+    constexpr int SETS = MI * NI < 4 ? (ONE ? 2 : 3) : 1;
+    f32x16 acc[SETS][MI][NI];
+#pragma unroll
+    for (int e = 0; e < SETS; ++e)
 #pragma unroll
         for (int x = 0; x < MI; ++x)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) l[x][h] = *reinterpret_cast<const f16x8*>(lds + place * GROUP + l_at + x * 4096 + c_at[stage][h]);
-    };
-
-    f32x16 acc[MI][NI];
+            for (int y = 0; y < NI; ++y)
 #pragma unroll
-    for (int x = 0; x < MI; ++x)
-#pragma unroll
-        for (int y = 0; y < NI; ++y)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[x][y][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) acc[e][x][y][r] = 0.0f;
 
 #pragma unroll
     for (int p = 0; p < RING; ++p)
@@ -304,29 +479,33 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_product(const Batch batch, c
         for (int c = 0; c < CP; ++c) copy(c, p, p);
     wait_for<(RING - 1) * CP>();
     meet();
-    f16x8 l0[MI][2], r0[NI][2], l1[MI][2], r1[NI][2];
+    f16x8 l0[S][MI][2], r0[S][NI][2], l1[S][MI][2], r1[S][NI][2];
     read(l0, r0, 0, 0);
 
-    // Group g + RING is copied in the second stage of group g, into g's place, and has landed
-    // when its first fragments are read, in the second stage of group g + RING - 1.
+    // Unit g + RING is copied in the last stage of unit g, into g's place, and has landed
+    // when its first fragments are read, in the last stage of unit g + RING - 1.
     int g = 0, place = 0;
-    auto stage = [&](auto second, auto& l, auto& r, auto& ln, auto& rn) {
-        constexpr int G = decltype(second)::value;
+    auto stage = [&](auto of_unit, auto products, auto& l, auto& r, auto& ln, auto& rn) {
+        constexpr int G = decltype(of_unit)::value, PRODUCTS = decltype(products)::value;
         const int next = G ? (place == RING - 1 ? 0 : place + 1) : place;
         if constexpr (G == 1) {
-            wait_for<(RING - 2) * CP>();                     // the next group has landed
+            wait_for<(RING - 2) * CP>();                     // the next unit has landed
             wait_reads();                                    // and nobody reads this one any more
             meet();
             __builtin_amdgcn_sched_barrier(0);
         }
-        read(ln, rn, next, 1 - G);
+        read(ln, rn, next, S == 2 ? 0 : 1 - G);
         __builtin_amdgcn_sched_barrier(0);
-        constexpr int SLOTS = 3 * MI;
+        constexpr int SLOTS = S * PRODUCTS * MI;
 #pragma unroll
         for (int t = 0; t < SLOTS; ++t) {
-            const int x = t % MI, h = t / MI;                // hi hi, then hi lo, then lo hi
+            // hi hi, then hi lo, then lo hi; or the hi hi of either group
+            const int x = t % MI, h = t / MI % PRODUCTS, k = t / MI / PRODUCTS, hl = ONE ? h : h == 2, hr = ONE ? h : h == 1;
 #pragma unroll
-            for (int y = 0; y < NI; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(r[y][h == 1], l[x][h == 2], acc[x][y], 0, 0, 0);
+            for (int y = 0; y < NI; ++y) {
+                f32x16& sum = acc[SETS > 1 ? h : 0][x][y];
+                sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(r[k][y][hr], l[k][x][hl], sum, 0, 0, 0);
+            }
             if constexpr (G == 1) {
 #pragma unroll
                 for (int c = t * CP / SLOTS; c < (t + 1) * CP / SLOTS; ++c) copy(c, g + RING, place);
@@ -337,141 +516,57 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_product(const Batch batch, c
     };
     constexpr std::integral_constant<int, 0> k0{};
     constexpr std::integral_constant<int, 1> k1{};
-    for (; g < groups; ++g) {
-        stage(k0, l0, r0, l1, r1);
-        stage(k1, l1, r1, l0, r0);
+    constexpr std::integral_constant<int, ONE ? 2 : 3> all{};
+    // (the last group of hi halves may have no second)
+    const int whole = ONE ? groups / 2 : groups;
+    if constexpr (S == 1) {
+        for (; g < whole; ++g) {
+            stage(k0, all, l0, r0, l1, r1);
+            stage(k1, all, l1, r1, l0, r0);
+        }
+        if (ONE && g < units) {
+            stage(k0, k1, l0, r0, l1, r1);
+            stage(k1, k1, l1, r1, l0, r0);
+        }
+    } else {
+        for (; g + 1 < whole; ++g) {
+            stage(k1, all, l0, r0, l1, r1);
+            ++g;
+            stage(k1, all, l1, r1, l0, r0);
+        }
+        if (g < whole) {
+            stage(k1, all, l0, r0, l1, r1);
+            ++g;
+            if (ONE && g < units) stage(k1, k1, l1, r1, l0, r0);
+        } else if (ONE && g < units) {
+            stage(k1, k1, l0, r0, l1, r1);
+        }
     }
     wait_for<0>();
     wait_reads();
     meet();                                                  // LDS is free
 
-    // Results go through LDS, a row of fragments at a time in a region of the wave's own, and
-    // leave by rows and transposed.
-    constexpr int COLS = NI * 32, QUADS = COLS / 4;
+    // Results go through LDS, a row of fragments at a time in a region of the wave's own.
+    constexpr int COLS = NI * 32;
     static_assert(NW * 32 * COLS * 4 <= RING * GROUP, "the results' regions must fit");
     float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * COLS;
-    const int row0 = i0 + wm * MI * 32, col0 = j0 + wn * COLS;
-    const bool turned = KIND >= LAST_F32 && ends.turned[w];
 #pragma unroll
     for (int x = 0; x < MI; ++x) {
 #pragma unroll
-        for (int y = 0; y < NI; ++y)
+        for (int y = 0; y < NI; ++y) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int quad = 8 * y + 2 * r + half;
-                *reinterpret_cast<float4*>(mine + i * COLS + ((quad ^ i) & (QUADS - 1)) * 4) =
-                    make_float4(acc[x][y][4 * r], acc[x][y][4 * r + 1], acc[x][y][4 * r + 2], acc[x][y][4 * r + 3]);
-            }
+            for (int e = SETS - 2; e >= 0; --e) acc[e][x][y] += acc[e + 1][x][y];   // the small ones first
+            lay<COLS>(mine, y, acc[0][x][y]);
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        // by rows: eight columns a lane
-        constexpr int PER_ROW = COLS / 8, AT_ONCE = 64 / PER_ROW;
-        if (!turned) {
-#pragma unroll
-            for (int p = 0; p < 32 / AT_ONCE; ++p) {
-                const int r = p * AT_ONCE + lane / PER_ROW, c = lane % PER_ROW * 8, row = row0 + x * 32 + r, col = col0 + c;
-                float v[8];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float4* const at = reinterpret_cast<float4*>(mine + r * COLS + (((c / 4 + q) ^ r) & (QUADS - 1)) * 4);
-                    const float4 f = *at;
-                    v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
-                }
-                if (row >= rows_l) continue;
-                if constexpr (KIND == GRAM_PART) {
-                    float* const to = reinterpret_cast<float*>(ws + at_parts(s)) + (static_cast<long long>(part) * s.n + row) * (mu_groups(s.n) * 32) + col;
-                    if (col < mu_groups(s.n) * 32) {
-                        reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                        reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
-                    }
-                } else if constexpr (KIND == LAST_F32 || KIND == LAST_BF16) {
-                    constexpr bool BF16 = KIND == LAST_BF16;
-                    const float by = ends.scale[w] / (SP * SX);
-                    const long long at = static_cast<long long>(row) * s.m + col;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] *= by;
-                    if (col + 8 <= s.m) {
-                        store_out<BF16>(ends.out[w], at, v);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            if (col + q < s.m) store1<BF16>(ends.out[w], at + q, v[q]);
-                    }
-                } else {
-                    if constexpr (KIND == GRAM) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] *= SA / (SX * SX);
-                    } else if constexpr (KIND == APPLY) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] *= 1.0f / SP;
-                    } else {
-                        // c A^2 + b A + a I, all times SP
-                        float old[8] = {};
-                        if (col < s.n) {
-                            const char* const from = ws + at_a(s) + row * mu_groups(s.n) * 128 + (col >> 5) * 128ll + (col & 31) * 2;
-                            const f16x8 hi = *reinterpret_cast<const f16x8*>(from), lo = *reinterpret_cast<const f16x8*>(from + 64);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) old[q] = static_cast<float>(hi[q]) + static_cast<float>(lo[q]);
-                        }
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            v[q] = cc * (SP / (SA * SA)) * v[q] + cb * (SP / SA) * old[q];
-                            if (row == col + q) v[q] += ca * SP;
-                        }
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)          // for the transposed form
-                            *reinterpret_cast<float4*>(mine + r * COLS + (((c / 4 + q) ^ r) & (QUADS - 1)) * 4) =
-                                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                    }
-                    const int cols = SYMMETRIC ? s.n : s.m;
-                    char* const to = ws + (KIND == GRAM ? at_a(s) : KIND == POLY ? at_p(s) : at_x(s));
-                    put8(to + row * mu_groups(cols) * 128, col, cols, v);
-                }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        }
-        // transposed: a column a lane, its 32 rows one group
-        const bool mirror = KIND == APPLY || ((KIND == GRAM || KIND == POLY) && I != J) || turned;
-        if (KIND != GRAM_PART && mirror) {
-#pragma unroll
-            for (int p = 0; p < (COLS + 63) / 64; ++p) {
-                const int c = p * 64 + (COLS < 64 ? i : lane), col = col0 + c, row = row0 + x * 32;
-                if (col >= rows_r || row >= rows_l || (COLS < 64 && half)) continue;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int r = 8 * k + q;
-                        v[q] = mine[r * COLS + (((c >> 2) ^ r) & (QUADS - 1)) * 4 + (c & 3)];
-                        if constexpr (KIND == GRAM) v[q] *= SA / (SX * SX);
-                        if constexpr (KIND == APPLY) v[q] *= 1.0f / SP;
-                    }
-                    if constexpr (KIND == LAST_F32 || KIND == LAST_BF16) {
-                        constexpr bool BF16 = KIND == LAST_BF16;
-                        const float by = ends.scale[w] / (SP * SX);
-                        const long long at = static_cast<long long>(col) * s.n + row + 8 * k;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] *= by;
-                        if (row + 8 * k + 8 <= s.n) {
-                            store_out<BF16>(ends.out[w], at, v);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                if (row + 8 * k + q < s.n) store1<BF16>(ends.out[w], at + q, v[q]);
-                        }
-                    } else {
-                        char* const to = ws + (KIND == GRAM ? at_a(s) : KIND == POLY ? at_p(s) : at_xt(s, 1 - turn));
-                        put8(to + col * mu_groups(s.n) * 128, row + 8 * k, s.n, v);
-                    }
-                }
-            }
-        }
+        emit<KIND, COLS>(mine, b, b.i0 + (wm * MI + x) * 32, b.j0 + wn * COLS, ends, ws, turn, ca, cb, cc);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
-// A from the parts of its k, added in order: 64 x 64 entries on or below the diagonal.
-__global__ __launch_bounds__(256) void muon_join(const Batch batch, char* ws, int tile) {
+// A from the parts of its k, added in order: 64 x 64 entries on or below the diagonal.  On it
+// the entries above are those below (the parts may not have them).
+__global__ __launch_bounds__(256) void muon_join(const Batch batch, char* ws) {
     __shared__ float sums[64][65];
     const int w = find_segment(batch.begin, batch.count, blockIdx.x);
     const Shape s = batch.s[w];
@@ -479,15 +574,15 @@ __global__ __launch_bounds__(256) void muon_join(const Batch batch, char* ws, in
     int I, J;
     below_diagonal(blockIdx.x - batch.begin[w], I, J);
     const int i0 = I * 64, j0 = J * 64;
-    const long long ld = mu_groups(s.n) * 32, stride = s.n * ld;
+    const long long ld = mu_groups(s.n) * 32, stride = s.n * ld, pitch = mu_groups(s.n) * 128;
     const float* const from = reinterpret_cast<const float*>(ws + at_parts(s));
     char* const to = ws + at_a(s);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         const int place = p * 256 + threadIdx.x, r = place >> 3, c = (place & 7) * 8, row = i0 + r, col = j0 + c;
         float v[8] = {};
-        // above the diagonal, within tiles of the product that have it, the parts are there too
-        if (row < s.n && col < ld) {
+        if (row < s.n && col <= row) {
+#pragma unroll 4
             for (int k = 0; k < parts; ++k) {
                 const float4* q = reinterpret_cast<const float4*>(from + k * stride + row * ld + col);
                 const float4 a = q[0], b = q[1];
@@ -496,22 +591,23 @@ __global__ __launch_bounds__(256) void muon_join(const Batch batch, char* ws, in
             }
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            v[q] *= SA / (SX * SX);
-            sums[r][c + q] = v[q];
-        }
-        if (row < s.n) put8(to + row * mu_groups(s.n) * 128, col, s.n, v);
+        for (int q = 0; q < 8; ++q) sums[r][c + q] = v[q] * (SA / (SX * SX));
     }
-    if (I == J) return;
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         const int place = p * 256 + threadIdx.x, r = place >> 3, c = (place & 7) * 8;
-        if (j0 + r >= s.n) continue;
         float v[8];
+        if (i0 + r < s.n) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = sums[c + q][r];
-        put8(to + (j0 + r) * mu_groups(s.n) * 128, i0 + c, s.n, v);
+            for (int q = 0; q < 8; ++q) v[q] = I == J && c + q > r ? sums[c + q][r] : sums[r][c + q];
+            put8(to + (i0 + r) * pitch, j0 + c, s.n, v);
+        }
+        if (I != J && j0 + r < s.n) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = sums[c + q][r];
+            put8(to + (j0 + r) * pitch, i0 + c, s.n, v);
+        }
     }
 }
 
@@ -525,14 +621,78 @@ bool mat_ok(const gc_muon_mat& a) {
     return a.n >= 1 && a.m >= 1 && a.n <= MU_MAX_SIDE && a.m <= MU_MAX_SIDE && static_cast<int64_t>(a.n) * a.m <= INT32_MAX;
 }
 
-// How the matrices of one launch are cut: parts of k for A = X X^T.
+// The tile that a workgroup takes.
+enum Way { TILE_64, TILE_128, TILE_128_PAIRED, TILE_192, TILE_256, WAYS };
+constexpr int SIDE[WAYS] = {64, 128, 128, 192, 256};
+
+int64_t parts_of(const Shape& s, int per) { return (mu_groups(s.m) + per - 1) / per; }
+
+int64_t blocks_of(int kind, Way way, const Shape& s, int per) {
+    return symmetric(kind) ? triangle(s.n, SIDE[way]) * (kind == GRAM ? parts_of(s, per) : 1) : tiles_of(s.n, s.m, SIDE[way], SIDE[way]);
+}
+
+// A launch's time in us, by fits to measurements over matrices of 64 x 576 to 4096 x 4096,
+// alone and in sets: START, a tile's start and end, and what a group takes a workgroup alone
+// and with every compute unit busy (the copies out of the L2 bound the smallest tile, the
+// matrix units at the clock that the power allows the largest).  Both sides of some
+// choices, X X^T and P X: 64 x 576 6.4 and 5.2 (64), 12.1 and 6.3 (128); 1024 x 1024 13.1 and
+// 13.4 (64), 20.8 and 22.2 (128), 26.8 and 27.0 (paired); 2048 x 2048 46 and 65 (64), 48 and 56
+// (128), 58 and 65 (paired), 81 and 85 (192); 4096 x 4096 329 and 515 (64), 238 and 349
+// (paired), 194 and 366 (192), 246 and 321 (256).  256 x 256 is not offered to A and P, whose
+// triangles it fills worst.
+double time_of(int kind, Way way, const Shape* shapes, const int* per, int count) {
+    constexpr double START = 3.0, FIXED[WAYS] = {3.0, 4.5, 5.5, 12.5, 19.0}, ALONE[WAYS] = {0.2, 0.43, 0.57, 0.85, 1.4},
+                     BUSY[WAYS] = {0.28, 0.66, 0.62, 1.35, 2.35};
+    constexpr bool PAIRED[WAYS] = {true, false, true, false, false};
+    double blocks = 0, work = 0, longest = 0, bytes = 0;
+    for (int w = 0; w < count; ++w) {
+        const double b = blocks_of(kind, way, shapes[w], per[w]), n = shapes[w].n;
+        const double g = kind == GRAM ? std::min<int64_t>(per[w], mu_groups(shapes[w].m)) : mu_groups(shapes[w].n);
+        blocks += b;
+        work += b * g;
+        longest = std::max(longest, g);
+        if (kind == GRAM && parts_of(shapes[w], per[w]) > 1) bytes += parts_of(shapes[w], per[w]) * n * n * 4;
+    }
+    const double x = blocks / 256, rounds = way == TILE_64 ? std::max(1.0, x) : std::ceil(x);
+    const double alone = longest * (ALONE[way] + (BUSY[way] - ALONE[way]) * std::min(1.0, x));
+    const double busy = work / blocks * BUSY[way] * rounds;
+    const double fixed = FIXED[way] * std::ceil(x / (PAIRED[way] ? 2 : 1));
+    return START + fixed + std::max(alone, x > 1 ? busy : 0.0) + (bytes > 0 ? 4.5 + bytes / 4e6 : 0.0);   // with the join
+}
+
+// How the matrices of one launch are cut: the tile of each product, and for A = X X^T the
+// groups of a part, so that few tiles of a long k do not leave the chip idle, nor long ones
+// run on behind the others.
 struct Cut {
+    Way way[3];                                              // A, P, P X
     int per[MU_MAX];
-    bool parts;
 };
 Cut cut_of(const gc_muon_mat* mats, int count) {
-    Cut cut = {};
-    for (int w = 0; w < count; ++w) cut.per[w] = static_cast<int>(mu_groups(oriented(mats[w]).m));
+    Shape shapes[MU_MAX];
+    Cut cut;
+    int per[MU_MAX];
+    int64_t longest = 0;
+    for (int w = 0; w < count; ++w) {
+        shapes[w] = oriented(mats[w]);
+        longest = std::max(longest, mu_groups(shapes[w].m));
+    }
+    for (int kind : {GRAM, POLY, APPLY}) {
+        double least = INFINITY;
+        for (int64_t most = longest;; most = (most + 1) / 2) {   // groups of a part
+            for (int w = 0; w < count; ++w) {
+                const int64_t g = mu_groups(shapes[w].m), parts = std::min<int64_t>(MU_MAX_PARTS, (g + most - 1) / most);
+                per[w] = static_cast<int>((g + parts - 1) / parts);
+            }
+            for (int way = 0; way < (symmetric(kind) ? TILE_256 : WAYS); ++way) {
+                const double us = time_of(kind, static_cast<Way>(way), shapes, per, count);
+                if (us >= least) continue;
+                least = us;
+                cut.way[kind] = static_cast<Way>(way);
+                if (kind == GRAM) std::copy(per, per + count, cut.per);
+            }
+            if (kind != GRAM || most <= 8) break;
+        }
+    }
     return cut;
 }
 
@@ -541,14 +701,14 @@ int64_t layout(const gc_muon_mat* mats, int count, const Cut& cut, Shape* shapes
     int64_t sums = 0;
     for (int w = 0; w < count; ++w) {
         if (partial) partial[w] = static_cast<int>(sums);
-        sums += (static_cast<int64_t>(mats[w].n) * mats[w].m + MU_TILE - 1) / MU_TILE;
+        sums += mu_sums(static_cast<int64_t>(mats[w].n) * mats[w].m);
     }
     int64_t at = static_cast<int64_t>(round_up(sums * 8, 1024));
     for (int w = 0; w < count; ++w) {
         Shape s = oriented(mats[w]);
         s.base = at;
         if (shapes) shapes[w] = s;
-        const int64_t parts = (mu_groups(s.m) + cut.per[w] - 1) / cut.per[w];
+        const int64_t parts = parts_of(s, cut.per[w]);
         at = at_parts(s) + (parts > 1 ? parts * s.n * mu_groups(s.n) * 128 : 0);
     }
     return at;
@@ -591,18 +751,41 @@ bool coefs_ok(const float* coefs, int steps) {
     return true;
 }
 
-template <int BM, int BN, int WM, int WN, int RING, int KIND>
-void launch_product(Batch& batch, const Ends& ends, char* ws, int turn, const float* c, hipStream_t s) {
-    constexpr bool SYMMETRIC = KIND == GRAM || KIND == GRAM_PART || KIND == POLY;
+template <int KIND, bool ONE>
+void launch_product(Way way, Batch& batch, const Ends& ends, char* ws, int turn, const float* c, hipStream_t s) {
     int64_t blocks = 0;
     for (int w = 0; w < batch.count; ++w) {
-        const Shape& m = batch.s[w];
         batch.begin[w] = static_cast<int>(blocks);
-        const int64_t parts = KIND == GRAM_PART ? (mu_groups(m.m) + batch.per[w] - 1) / batch.per[w] : 1;
-        blocks += SYMMETRIC ? triangle(m.n, BM) * parts : tiles_of(m.n, m.m, BM, BN);
+        blocks += blocks_of(KIND, way, batch.s[w], batch.per[w]);
     }
-    TimedLaunch tl("muon_product", s);
-    muon_product<BM, BN, WM, WN, RING, KIND><<<static_cast<unsigned>(blocks), WM * WN * 64, 0, s>>>(batch, ends, ws, turn, c[0], c[1], c[2]);
+    const unsigned grid = static_cast<unsigned>(blocks);
+    TimedLaunch tl("muon_tile", s);
+    auto go = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, s>>>(batch, ends, ws, turn, c[0], c[1], c[2]); };
+    switch (way) {
+        case TILE_64: go(muon_tile<64, 64, 2, 2, 4, KIND, ONE>, 256); break;
+        case TILE_128: go(muon_tile<128, 128, 2, 4, 4, KIND, ONE>, 512); break;
+        case TILE_128_PAIRED: go(muon_tile<128, 128, 2, 2, 2, KIND, ONE>, 256); break;
+        case TILE_192: go(muon_tile<192, 192, 2, 2, 3, KIND, ONE>, 256); break;
+        default:
+            if constexpr (!symmetric(KIND)) go(muon_tile<256, 256, 2, 2, 2, KIND, ONE>, 256);
+    }
+}
+
+// A of the matrices whose products are in parts.
+void launch_join(const Batch& all, char* ws, hipStream_t s) {
+    Batch batch;
+    batch.count = 0;
+    int64_t blocks = 0;
+    for (int w = 0; w < all.count; ++w) {
+        if (parts_of(all.s[w], all.per[w]) == 1) continue;
+        batch.s[batch.count] = all.s[w];
+        batch.per[batch.count] = all.per[w];
+        batch.begin[batch.count++] = static_cast<int>(blocks);
+        blocks += triangle(all.s[w].n, 64);
+    }
+    if (batch.count == 0) return;
+    TimedLaunch tl("muon_join", s);
+    muon_join<<<static_cast<unsigned>(blocks), 256, 0, s>>>(batch, ws);
 }
 
 int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float beta, int nesterov, int steps, const float* coefs,
@@ -623,7 +806,7 @@ int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float
         src.m[w] = a.m;
         src.base[w] = batch.s[w].base;
         src.begin[w] = static_cast<int>(sums);
-        sums += (static_cast<int64_t>(a.n) * a.m + MU_TILE - 1) / MU_TILE;
+        sums += mu_sums(static_cast<int64_t>(a.n) * a.m);
         begin[w] = static_cast<int>(tiles);
         tiles += tiles_of(a.n, a.m, 64, 64);
         batch.per[w] = cut.per[w];
@@ -648,11 +831,14 @@ int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float
     rc = check_launch("gc_muon_step");
     for (int k = 0; k < steps && rc == GC_OK; ++k) {
         const float* c = coefs ? coefs + 3 * k : MU_COEFS;
-        launch_product<128, 128, 2, 2, 2, GRAM>(batch, ends, ws, k & 1, c, s);
-        launch_product<128, 128, 2, 2, 2, POLY>(batch, ends, ws, k & 1, c, s);
-        if (k + 1 < steps) launch_product<128, 128, 2, 2, 2, APPLY>(batch, ends, ws, k & 1, c, s);
-        else if (out_dtype == GC_BF16) launch_product<128, 128, 2, 2, 2, LAST_BF16>(batch, ends, ws, k & 1, c, s);
-        else launch_product<128, 128, 2, 2, 2, LAST_F32>(batch, ends, ws, k & 1, c, s);
+        const bool last = k + 1 == steps, one = last && out_dtype == GC_BF16;
+        if (one) launch_product<GRAM, true>(cut.way[0], batch, ends, ws, k & 1, c, s);
+        else launch_product<GRAM, false>(cut.way[0], batch, ends, ws, k & 1, c, s);
+        launch_join(batch, ws, s);
+        launch_product<POLY, false>(cut.way[1], batch, ends, ws, k & 1, c, s);
+        if (!last) launch_product<APPLY, false>(cut.way[2], batch, ends, ws, k & 1, c, s);
+        else if (one) launch_product<LAST_BF16, true>(cut.way[2], batch, ends, ws, k & 1, c, s);
+        else launch_product<LAST_F32, false>(cut.way[2], batch, ends, ws, k & 1, c, s);
         rc = check_launch("gc_muon_step");
     }
     return rc;

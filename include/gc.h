@@ -532,10 +532,13 @@ size_t gc_muon_workspace_bytes(const gc_muon_mat* mats, int nmats);
  *   ws       >= gc_muon_workspace_bytes(mats, nmats) bytes
  * Sums are in float32 (the norm's in float64); X, A and a + b A + c A A are held as
  * pairs of 11-bit floating point numbers, 22 to 24 bits together and nothing below
- * 2^-37 (X's entries are at most 4), and rounded once to out.  The usual coefficients make what a step rounds up to 3.4 times
- * as large with every step that follows: a float32 out is within about 2e-4 of
- * the exact one (2-norm over the matrix's), and within 2e-6 to 2e-5 for matrices
- * whose singular values are not far apart.
+ * 2^-37 (X's entries are at most 4), and rounded once to out.  The usual
+ * coefficients make what a step rounds up to 3.4 times as large with every step
+ * that follows: a float32 out is within about 2e-4 of the exact one (2-norm over the
+ * matrix's), and within 2e-6 to 2e-5 for matrices whose singular values are not far
+ * apart.  For a bf16 out the last step, whose roundings nothing enlarges, takes
+ * X X^T and the product with X from the 11-bit parts alone, and is off by 2e-4 to 8e-4
+ * before the rounding to bf16, which is off by 1.7e-3.
  * Kernel launches only: no copy, no allocation, no synchronisation, so the call may
  * be captured in a HIP graph.  [host] arrays may be reused as soon as it returns.
  * Errors: GC_ERR_ARG (null or misaligned pointer, shape, steps or coefs out of

@@ -20,7 +20,13 @@ norm of the sum is at most the sum of the norms.  There (`steps_bound`) the roun
 taken as independent: in a product V W of k terms they are at most 3 * 2^-22 + sqrt(3 k) 2^-23
 of |V W| and of the root of the sum of its terms' squares, each in the Frobenius norm, and an error
 E of a factor is one of at most |E| times the other's largest singular value.  The tests take
-twice that too.  A bf16 result has 2^-8 of each entry more.
+twice that too.
+
+A bf16 result's last step takes A = X X^T and P X from the hi parts alone, each off by 2^-11 of
+itself at most.  Its result is off by 2^-11 times 2 |a| |X| (P's rounding and X's), 4 |b| |X||X|^T |X|
+(the two X of A as well) and 6 |c| (|X||X|^T)^2 |X| more, entry by entry; as independent roundings by
+(|b| + 2 |c| |A|_2) |X|_2 times 2 * 2^-11 of the root of the sum of X X^T's terms' squares, and 2^-11 of
+|P|_F |X|_2 + |P|_2 |X|_F.  Then 2^-8 of each entry for the rounding.
 """
 import numpy as np
 import pytest
@@ -94,7 +100,7 @@ def floors(x, big, p, b, c):
     return p @ dx + dp @ x
 
 
-def one_step_bound(u, coefs):
+def one_step_bound(u, coefs, bf16=False):
     """(the step's result, what it may be off by) in float64, n <= m or not."""
     x = np.asarray(u, np.float64)
     x = x / np.linalg.norm(x)
@@ -107,10 +113,14 @@ def one_step_bound(u, coefs):
     e = 9 * 2.0 ** -22 + 3 * (m + 2 * n) * 2.0 ** -23
     d = 9 * 2.0 ** -22 + (3 * n * 2.0 ** -23 if b or c else 0.0)
     bound = 2 * (e * (p @ np.abs(x)) + d * a * np.abs(x) + floors(np.abs(x), big, p + a * np.eye(n), b, c))
-    return oracle.newton_schulz(u, 1, coefs), bound.T if turned else bound
+    want = oracle.newton_schulz(u, 1, coefs)
+    if bf16:
+        bound += 2.0 ** -11 * 1.01 * (2 * a * np.abs(x) + (4 * b * big + 6 * c * (big @ big)) @ np.abs(x))
+    bound = bound.T if turned else bound
+    return want, bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want) if bf16 else bound
 
 
-def steps_bound(u, steps, coefs=USUAL):
+def steps_bound(u, steps, coefs=USUAL, bf16=False):
     """2-norm (Frobenius) by which `steps` steps may be off when roundings are independent."""
     x = np.asarray(u, np.float64)
     x = (x.T if x.shape[0] > x.shape[1] else x) / np.linalg.norm(x)
@@ -121,7 +131,7 @@ def steps_bound(u, steps, coefs=USUAL):
         return (3 * 2.0 ** -22 + (3 * k) ** 0.5 * 2.0 ** -23) * (norm(v @ w) + norm(np.sqrt((v * v) @ (w * w))))
 
     off = 0.0
-    for _ in range(steps):
+    for k in range(steps):
         n, m = x.shape
         g = x @ x.T
         gg = g @ g
@@ -133,9 +143,12 @@ def steps_bound(u, steps, coefs=USUAL):
         here = off_p * x2 + p2 * 2.0 ** -22 * norm(x) + product_off(p, x, n)
         big = np.abs(x) @ np.abs(x).T
         least = floors(np.abs(x), big, np.abs(p), abs(b), abs(c))
+        if bf16 and k == steps - 1:
+            one = 2.0 ** -10 * norm(np.sqrt((x * x) @ (x * x).T))
+            here += (abs(b) + 2 * abs(c) * g2) * one * x2 + 2.0 ** -11 * (norm(p) * x2 + p2 * norm(x))
         off = 4 * off + 2 * (here + norm(least))
         x = p @ x
-    return off
+    return off * (1 + 2.0 ** -8) + 2.0 ** -8 * norm(x) if bf16 else off
 
 
 SHAPES = [(1, 1), (1, 2), (2, 1), (1, 700), (700, 1), (3, 5), (31, 33), (32, 32), (33, 31), (64, 576), (576, 64), (63, 65), (65, 129),
@@ -153,7 +166,8 @@ def test_one_step(n, m, coefs):
         assert np.all(np.abs(got.numpy() - want) <= bound), kind
         assert np.linalg.norm(got.numpy() - want) <= steps_bound(u, 1, coefs), kind
         (got,), _ = step([u], steps=1, coefs=coefs, out_dtype=torch.bfloat16)
-        assert np.all(np.abs(got.double().numpy() - want) <= bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)), kind
+        assert np.all(np.abs(got.double().numpy() - want) <= one_step_bound(u, coefs, True)[1]), kind
+        assert np.linalg.norm(got.double().numpy() - want) <= steps_bound(u, 1, coefs, True), kind
 
 
 @pytest.mark.parametrize("n,m", [(3, 5), (33, 31), (300, 200)])
@@ -183,7 +197,7 @@ def test_five_steps(n, m, kind):
     (got,), _ = step([u])
     assert np.linalg.norm(got.numpy() - want) <= off
     (got,), _ = step([u], out_dtype=torch.bfloat16)
-    assert np.linalg.norm(got.double().numpy() - want) <= off * (1 + 2.0 ** -8) + 2.0 ** -8 * np.linalg.norm(want)
+    assert np.linalg.norm(got.double().numpy() - want) <= steps_bound(u, 5, bf16=True)
 
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 6])
@@ -367,8 +381,7 @@ def test_training_steps_in_8_bits():
         ref = oracle.muon_step(grad.cpu().numpy(), hmem, 0.9, True, scale=0.2)
         hmem = ref["mem"]
         assert np.array_equal(f32_bits(mem), f32_bits(hmem))
-        off = 0.2 * steps_bound(ref["u"], 5)
-        assert np.linalg.norm(update.double().cpu().numpy() - ref["out"]) <= off + 2.0 ** -8 * np.linalg.norm(ref["out"])
+        assert np.linalg.norm(update.double().cpu().numpy() - ref["out"]) <= 0.2 * steps_bound(ref["u"], 5, bf16=True)
         w -= 0.02 * update.float()
     # an orthogonalised update beside PowerSGD's factors: the same message through a rank-4 step
     q = to_dev(r.standard_normal((4, fi), dtype=np.float32))
@@ -378,7 +391,7 @@ def test_training_steps_in_8_bits():
     gc.gc_muon_step(again, 0.0, workspace(again))
     u = low.out.cpu().numpy()
     exact = oracle.newton_schulz(u)
-    assert np.linalg.norm(update.double().cpu().numpy() - exact) <= steps_bound(u, 5) + 2.0 ** -8 * np.linalg.norm(exact)
+    assert np.linalg.norm(update.double().cpu().numpy() - exact) <= steps_bound(u, 5, bf16=True)
 
 
 # ---------------------------------------------------------------- large
@@ -402,8 +415,8 @@ def test_past_32_bits():
     norm = norm.sqrt()
     for i in range(0, n, 4000):
         want = x[i:i + 4000].double() / norm
-        # 2^-8 for the rounding to bf16, the pair's 2^-22, and its least value's half, 2^-37 (P is 1: exact)
-        assert bool(((out[i:i + 4000].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want.abs() + 2.0 ** -36).all())
+        # 2^-8 for the rounding to bf16, 2^-11 for X's hi part, and its least value's half, 2^-37 (P is 1: exact)
+        assert bool(((out[i:i + 4000].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want.abs() + 2.0 ** -36).all())
     del x, out, ws, mats
     torch.cuda.empty_cache()
 

@@ -32,7 +32,7 @@ def test_sizes(gcl):  # noqa: F811
     assert size((G, M, O, 2**22, 511, 1.0)) > 0
     assert gcl.lib.gc_muon_workspace_bytes(None, 1) == 0
     assert gcl.lib.gc_muon_workspace_bytes(array(gcl, (G, M, O, 4, 4, 1.0)), 0) == 0
-    assert "muon_product" in gcl.gc_kernel_names()
+    assert "muon_tile" in gcl.gc_kernel_names()
 
 
 @no_gpu
