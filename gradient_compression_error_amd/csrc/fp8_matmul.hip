@@ -252,13 +252,17 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
     constexpr bool AHEAD = ADD && EARLY && R == 4;
     constexpr int COLS = NI * 32, WIDE = BF16 ? 8 : 4, PER_ROW = COLS / WIDE, AT_ONCE = 64 / PER_ROW;
     const int col = j0 + wn * COLS + (lane % PER_ROW) * WIDE, row0 = i0 + wm * (BM / WM) + lane / PER_ROW;
-    const bool inside = i0 + BM <= A.rows && j0 + BN <= B.rows;
+    const int rows_left = A.rows - row0;                     // rows of this lane's from row0 on
+    const bool whole = col + WIDE <= B.rows;                 // its 16 bytes are all there
     u32x4_any old[AHEAD ? MI : 1][32 / AT_ONCE];
-    if (AHEAD && inside) {
+    auto fetch = [&](int to, int x) {
 #pragma unroll
-        for (int x = 0; x < MI; ++x)
+        for (int t = 0; t < 32 / AT_ONCE; ++t)
+            if (whole && x * 32 + t * AT_ONCE < rows_left) old[to][t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
+    };
+    if constexpr (AHEAD) {
 #pragma unroll
-            for (int t = 0; t < 32 / AT_ONCE; ++t) old[x][t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
+        for (int x = 0; x < MI; ++x) fetch(x, x);
     }
 
     // Where this wave's copies come from: a uniform base per operand and a lane's
@@ -350,6 +354,14 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
 #pragma unroll
     for (int x = 0; x < MI; ++x) read(fa0[x], a_at + x * 4096, 0, 0);
 
+    bf16x8 wide_a[2][EXACT ? MI : 1], wide_b[2][EXACT ? NI : 1];
+    if constexpr (EXACT) {
+#pragma unroll
+        for (int y = 0; y < NI; ++y) wide_b[0][y] = widened(fb0[y][0], fb0[y][1], scale_operand<0>(sb[y]));
+#pragma unroll
+        for (int x = 0; x < MI; ++x) wide_a[0][x] = widened(fa0[x][0], fa0[x][1], scale_operand<0>(sa[x]));
+    }
+
     // One stage, the first or second (G) of a group, the Q-th of its chunk.  Group p + R
     // is copied from the second stage of group p on, into p's place, and has landed when
     // its first fragments are read, in the second stage of group p + R - 1.  Chunk c + 1
@@ -379,24 +391,33 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
         // The copies are spread over the matrix instructions: a wave that issues them
         // together waits for the address unit instead.
         if constexpr (EXACT) {
-            bf16x8 wide[NI];
+            // 16 columns of k a time.  The conversions of the next 16 (of the next stage, at the
+            // end) are spread over the matrix instructions of the present ones.
+            constexpr int PRODUCTS = MI * NI, FRAGMENTS = MI + NI, QN = G ? (Q + 1) & 3 : Q;
+            auto& sa_next = [&]() -> auto& { if constexpr (Q == 3 && G == 1) return san; else return sa; }();
+            auto& sb_next = [&]() -> auto& { if constexpr (Q == 3 && G == 1) return sbn; else return sb; }();
 #pragma unroll
-            for (int t = 0; t < 4 * MI; ++t) {               // 16 columns of k a time, fragment by fragment of A
-                const int p = t / MI, x = t % MI;
-                if (x == 0) {
+            for (int t = 0; t < 4 * PRODUCTS; ++t) {
+                const int p = t / PRODUCTS, j = t % PRODUCTS, x = j / NI, y = j % NI, n = (p + 1) & 3;
+                acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wide_b[p & 1][y], wide_a[p & 1][x], acc[x][y], 0, 0, 0);
 #pragma unroll
-                    for (int y = 0; y < NI; ++y) wide[y] = widened(fb[y][2 * p], fb[y][2 * p + 1], scale_operand<Q>(sb[y]));
+                for (int f = j * FRAGMENTS / PRODUCTS; f < (j + 1) * FRAGMENTS / PRODUCTS; ++f) {
+                    if (f < NI) {
+                        const i32x8& from = p < 3 ? fb[f] : fbn[f];
+                        wide_b[n & 1][f] = widened(from[2 * n], from[2 * n + 1], p < 3 ? scale_operand<Q>(sb[f]) : scale_operand<QN>(sb_next[f]));
+                    } else {
+                        const i32x8& from = p < 3 ? fa[f - NI] : fan[f - NI];
+                        wide_a[n & 1][f - NI] = widened(from[2 * n], from[2 * n + 1], p < 3 ? scale_operand<Q>(sa[f - NI]) : scale_operand<QN>(sa_next[f - NI]));
+                    }
                 }
-                const bf16x8 w = widened(fa[x][2 * p], fa[x][2 * p + 1], scale_operand<Q>(sa[x]));
-#pragma unroll
-                for (int y = 0; y < NI; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wide[y], w, acc[x][y], 0, 0, 0);
+                constexpr int SLOTS = 4 * PRODUCTS;
                 if constexpr (G == 1) {
 #pragma unroll
-                    for (int c = t * NOW / (4 * MI); c < (t + 1) * NOW / (4 * MI); ++c) copy_code(c, 4 * chunk + Q + R, HERE);
-                    if (Q == 0 && t == 4 * MI - 1) copy_scales(chunk + 1, (chunk + 1) & 1);
+                    for (int c = t * NOW / SLOTS; c < (t + 1) * NOW / SLOTS; ++c) copy_code(c, 4 * chunk + Q + R, HERE);
+                    if (Q == 0 && t == SLOTS - 1) copy_scales(chunk + 1, (chunk + 1) & 1);
                 } else {
 #pragma unroll
-                    for (int c = NOW + t * LATER / (4 * MI); c < NOW + (t + 1) * LATER / (4 * MI); ++c)
+                    for (int c = NOW + t * LATER / SLOTS; c < NOW + (t + 1) * LATER / SLOTS; ++c)
                         copy_code(c, 4 * chunk + Q - 1 + R, (Q + R - 1) % R);
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -479,10 +500,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
     float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * COLS;
 #pragma unroll
     for (int x = 0; x < MI; ++x) {
-        if (ADD && !AHEAD && inside) {
-#pragma unroll
-            for (int t = 0; t < 32 / AT_ONCE; ++t) old[0][t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
-        }
+        if constexpr (ADD && !AHEAD) fetch(0, x);
 #pragma unroll
         for (int y = 0; y < NI; ++y)
 #pragma unroll
@@ -503,10 +521,11 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
                 const float4 f = *reinterpret_cast<const float4*>(mine + r * COLS + ((quad ^ r) & (COLS / 4 - 1)) * 4);
                 v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
             }
-            if (inside) {
+            if (row >= A.rows) continue;
+            if (whole) {
                 if constexpr (ADD) add16<BF16>(v, old[AHEAD ? x : 0][t]);
                 store16<BF16, OUT != OUT_PART>(out, row * ldo + col, v);
-            } else if (row < A.rows) {
+            } else {
                 put<BF16, ADD, WIDE>(out, row * ldo + col, v, B.rows - col);
             }
         }
@@ -532,12 +551,19 @@ bool matmul_shape_ok(int64_t m, int64_t n, int64_t k) {
     return m <= MX_MAX_DIM && n <= MX_MAX_DIM && k <= MX_MAX_K && mx_shape_ok(m, k) && mx_shape_ok(n, k) && mx_shape_ok(m, n);
 }
 
-// The cheapest kernel by times (in us) fitted to measurements; a round is what 256 compute
-// units take at once.
+// The cheapest kernel by times (in us) fitted to measurements over m of 1 .. 8192, n of 512 ..
+// 8192 and k of 300 .. 16384, in graphs; a round is what 256 compute units take at once.
+// Both sides at some borders, bf16 out: 4 x 8192 x 8192 14.6 (1 x 1), 13.2 (1 x 2); 64 x 4096 x
+// 1024 5.6 (1 x 2), 4.9 (2 x 2), 5.8 (2 x 4); 777 x 1001 x 1155 10.0 (4 x 4), 8.4 (128); 1024 x
+// 1024 x 16384 47.9 (128), 27.3 (in four parts); 2048 x 4096 x 4096 37.1 (128), 34.2 (128, two a
+// unit), 47.0 (256); 4096 x 4096 x 4096 68.1 (two a unit), 55.6 (256).  float32 out: 1024 x
+// 1024 x 1024 8.8 (4 x 4), 10.6 (128), 10.2 (two a unit, each alone); 4096 x 1024 x 8192 62.6 (128),
+// 58.6 (two a unit, each alone).  256 x 256 is not for float32, whose operands' wide forms
+// leave it no registers.
 Plan plan_of(int64_t m, int64_t n, int64_t k, bool exact) {
     const int groups = static_cast<int>(mx_groups(k));
     const double g = groups;
-    Plan best = {Plan::TILE_256, 1, (groups + 3) / 4 * 4, (n + 3) / 4 * 4};
+    Plan best = {Plan::TILE_128_PAIRED, 1, (groups + 3) / 4 * 4, (n + 3) / 4 * 4};
     double least = INFINITY;
     auto offer = [&](Plan::Kind kind, double us, int splits) {
         if (us >= least) return;
@@ -554,22 +580,25 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool exact) {
         const double r = std::max(1.0, tiles / 256.0);
         offer(kind, 2.5 + per_group * g * (whole ? std::ceil(r) : r), 1);
     };
-    wave(Plan::WAVE_1_1, 1, 1, 0.14, false);
-    wave(Plan::WAVE_1_2, 1, 2, 0.21, false);
-    wave(Plan::WAVE_2_1, 2, 1, 0.2, false);
-    wave(Plan::WAVE_2_2, 2, 2, 0.28, false);
-    wave(Plan::WAVE_2_4, 2, 4, 0.45, true);
-    wave(Plan::WAVE_4_4, 4, 4, 0.8, true);
+    wave(Plan::WAVE_1_1, 1, 1, 0.12, false);
+    wave(Plan::WAVE_1_2, 1, 2, 0.17, false);
+    wave(Plan::WAVE_2_1, 2, 1, 0.18, false);
+    wave(Plan::WAVE_2_2, 2, 2, 0.23, false);
+    wave(Plan::WAVE_2_4, 2, 4, 0.36, true);
+    wave(Plan::WAVE_4_4, 4, 4, 0.67, true);
     // A part costs its write and read back, and a launch; at most 256 workgroups.
     const int64_t t128 = tiles_of(m, n, 128, 128), t256 = tiles_of(m, n, 256, 256);
-    for (int s = 1; s <= MAX_SPLITS && t128 * s <= 256 && (s == 1 || groups >= 16 * s); s *= 2) {
-        const double parts = s > 1 ? 5.0 + 0.55e-6 * 4.0 * s * static_cast<double>(m) * best.ldp : 0.0;
-        offer(Plan::TILE_128, 4.2 + (t128 * s > 128 ? 0.58 : 0.5) * std::ceil(g / s) + parts, s);
+    for (int s = 1; s <= MAX_SPLITS && t128 * s <= 256 && (s == 1 || groups >= 8 * s); s *= 2) {
+        const double parts = s > 1 ? 3.0 + 0.35e-6 * 4.0 * s * static_cast<double>(m) * best.ldp : 0.0;
+        const double one = exact ? (t128 * s > 128 ? 0.88 : 0.67) : (t128 * s > 128 ? 0.42 : 0.34);
+        offer(Plan::TILE_128, (exact ? 5.5 : 4.8) + one * std::ceil(g / s) + parts, s);
     }
     auto rounds = [](double x) { return x <= 1 ? 1.0 : (x + std::ceil(x)) / 2; };
     if (t128 > 256) {
-        offer(Plan::TILE_128_PAIRED, rounds(t128 / 512.0) * (3.5 + 1.25 * g), 1);
-        offer(Plan::TILE_256, rounds(t256 / 256.0) * (8.0 + 1.85 * g), 1);
+        offer(Plan::TILE_128_PAIRED, rounds(t128 / 512.0) * (exact ? 5.0 + 1.58 * g : 4.5 + 0.95 * g), 1);
+        if (!exact) offer(Plan::TILE_256, rounds(t256 / 256.0) * (8.0 + 1.48 * g), 1);
+    } else if (exact) {
+        offer(Plan::TILE_128_PAIRED, 5.2 + (t128 > 128 ? 0.83 : 0.68) * g, 1);
     }
     return best;
 }
@@ -582,9 +611,9 @@ void launch_wave(const Operand& A, const Operand& B, int groups, int sp, void* o
     else fp8_wave<MI, NI, W, GU, true><<<grid, W * 64, 0, s>>>(A, B, groups, sp, out, ldo, add);
 }
 
-template <int BM, int BN, int WM, int WN, int R>
-void launch_tile(const Plan& p, const Operand& A, const Operand& B, int groups, int sp, void* out, int64_t ldo, int dtype, int add,
-                 void* ws, hipStream_t s) {
+template <int BM, int BN, int WM, int WN, int R, bool EXACT>
+void launch_tile(const Plan& p, const Operand& A, const Operand& B, int groups, int sp, void* out, int64_t ldo, int add, void* ws,
+                 hipStream_t s) {
     const unsigned grid = static_cast<unsigned>(tiles_of(A.rows, B.rows, BM, BN) * p.splits);
     const int64_t part = A.rows * p.ldp;
     TimedLaunch tl("fp8_tile", s);
@@ -592,16 +621,11 @@ void launch_tile(const Plan& p, const Operand& A, const Operand& B, int groups, 
         kernel<<<grid, WM * WN * 64, 0, s>>>(A, B, groups, sp, p.per_split, to, ld, stride);
     };
     if (p.splits > 1) {
-        if constexpr (BM == 128 && R == 4) {                 // only this one is split
-            if (dtype == GC_BF16) go(fp8_tile<BM, BN, WM, WN, R, OUT_PART, false>, ws, p.ldp, part * 4);
-            else go(fp8_tile<BM, BN, WM, WN, R, OUT_PART, true>, ws, p.ldp, part * 4);
-        }
-    } else if (dtype == GC_BF16) {
-        if (add) go(fp8_tile<BM, BN, WM, WN, R, OUT_BF16_ADD, false>, out, ldo, 0);
-        else go(fp8_tile<BM, BN, WM, WN, R, OUT_BF16, false>, out, ldo, 0);
+        if constexpr (BM == 128 && R == 4) go(fp8_tile<BM, BN, WM, WN, R, OUT_PART, EXACT>, ws, p.ldp, part * 4);   // only this one is split
+    } else if (add) {
+        go(fp8_tile<BM, BN, WM, WN, R, EXACT ? OUT_F32_ADD : OUT_BF16_ADD, EXACT>, out, ldo, 0);
     } else {
-        if (add) go(fp8_tile<BM, BN, WM, WN, R, OUT_F32_ADD, true>, out, ldo, 0);
-        else go(fp8_tile<BM, BN, WM, WN, R, OUT_F32, true>, out, ldo, 0);
+        go(fp8_tile<BM, BN, WM, WN, R, EXACT ? OUT_F32 : OUT_BF16, EXACT>, out, ldo, 0);
     }
 }
 
@@ -662,9 +686,15 @@ int gc_fp8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int a_block_r
         case Plan::WAVE_2_2: launch_wave<2, 2, 8, 4>(A, B, groups, sp, out, ldo, out_dtype, accumulate, s); break;
         case Plan::WAVE_2_4: launch_wave<2, 4, 8, 2>(A, B, groups, sp, out, ldo, out_dtype, accumulate, s); break;
         case Plan::WAVE_4_4: launch_wave<4, 4, 4, 2>(A, B, groups, sp, out, ldo, out_dtype, accumulate, s); break;
-        case Plan::TILE_128: launch_tile<128, 128, 2, 4, 4>(p, A, B, groups, sp, out, ldo, out_dtype, accumulate, ws, s); break;
-        case Plan::TILE_128_PAIRED: launch_tile<128, 128, 2, 2, 2>(p, A, B, groups, sp, out, ldo, out_dtype, accumulate, ws, s); break;
-        case Plan::TILE_256: launch_tile<256, 256, 2, 2, 2>(p, A, B, groups, sp, out, ldo, out_dtype, accumulate, ws, s); break;
+        case Plan::TILE_128:
+            if (out_dtype == GC_BF16) launch_tile<128, 128, 2, 2, 4, false>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);
+            else launch_tile<128, 128, 2, 4, 4, true>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);
+            break;
+        case Plan::TILE_128_PAIRED:
+            if (out_dtype == GC_BF16) launch_tile<128, 128, 2, 2, 2, false>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);
+            else launch_tile<128, 128, 2, 2, 2, true>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);
+            break;
+        case Plan::TILE_256: launch_tile<256, 256, 2, 2, 2, false>(p, A, B, groups, sp, out, ldo, accumulate, ws, s); break;
     }
     rc = check_launch(fn);
     if (rc != GC_OK || p.splits == 1) return rc;
