@@ -34,8 +34,8 @@
 namespace gc {
 namespace {
 
-constexpr int MU_MAX = 64;             // matrices of a launch
-constexpr int MU_SUMS = 512;           // partial sums of squares of a matrix, at most
+constexpr int MU_MAX = 32;             // matrices of a launch: their table fits a launch's arguments
+constexpr int MU_SUMS = 1024;          // partial sums of squares of a matrix, at most
 constexpr int64_t MU_MAX_SIDE = int64_t(1) << 22;
 constexpr int MU_MAX_STEPS = 32;
 constexpr int MU_MAX_PARTS = 64;
@@ -67,27 +67,26 @@ __host__ __device__ inline int mu_chunk(long long entries) {
 }
 __host__ __device__ inline int mu_sums(long long entries) { return static_cast<int>((entries + mu_chunk(entries) - 1) / mu_chunk(entries)); }
 
-// One launch's work: workgroups begin[i] .. are matrix i's.
-struct Batch {
-    Shape s[MU_MAX];
-    int begin[MU_MAX];
-    int per[MU_MAX];                                         // groups of k of a part (A = X X^T)
-    int count;
-};
-struct Ends {
-    void* out[MU_MAX];
-    float scale[MU_MAX];
-    unsigned char turned[MU_MAX];                            // X is the transposed matrix
-};
-struct Sources {
+enum { GRAM, POLY, APPLY, LAST_F32, LAST_BF16 };
+constexpr bool symmetric(int kind) { return kind == GRAM || kind == POLY; }
+
+// A call's matrices.  The first kernel gets the table as an argument and leaves it at the
+// workspace's start for the others: 17 launches with 2.4 KB of arguments each took the host 82
+// us.  Workgroups from `..._at[i]` on are matrix i's.
+struct Table {
     const void* grad[MU_MAX];
     float* mem[MU_MAX];
-    int n[MU_MAX], m[MU_MAX];                                // as given
-    int begin[MU_MAX];
-    int partial[MU_MAX];                                     // the first of its partial sums
-    long long base[MU_MAX];
+    void* out[MU_MAX];
+    Shape s[MU_MAX];
+    int sums_at[MU_MAX], start_at[MU_MAX], tile_at[3][MU_MAX], join_at[MU_MAX];
+    int per[MU_MAX];                                         // groups of k of a part (A = X X^T)
+    float scale[MU_MAX];
+    unsigned char turned[MU_MAX];                            // X is the transposed matrix
     int count;
 };
+static_assert(sizeof(Table) % 4 == 0 && sizeof(Table) <= 4096 - 64, "a launch's arguments are at most 4 KB");
+constexpr int64_t SUMS_AT = (sizeof(Table) + 1023) / 1024 * 1024;   // the partial sums, behind the table
+constexpr int tile_kind(int kind) { return kind < APPLY ? kind : APPLY; }
 
 // Eight values as pairs: two conversions and a mixed subtraction for two of them.
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -128,12 +127,16 @@ __device__ __forceinline__ float direction(float mem, float beta, float g, bool 
 
 // mem = beta mem + grad, and the sum of u^2 over a chunk of the entries in float64.
 template <bool BF16>
-__global__ __launch_bounds__(256) void muon_moment(const Sources src, float beta, int nesterov, double* partial) {
+__global__ __launch_bounds__(256) void muon_moment(const Table table, float beta, int nesterov, char* ws) {
     __shared__ double sums[4];
-    const int w = find_segment(src.begin, src.count, blockIdx.x), chunk = blockIdx.x - src.begin[w];
-    const void* const grad = src.grad[w];
-    float* const mem = src.mem[w];
-    const long long count = static_cast<long long>(src.n[w]) * src.m[w], size = mu_chunk(count), first = chunk * size;
+    if (blockIdx.x == 0) {
+        for (unsigned i = threadIdx.x; i < sizeof(Table) / 4; i += 256)
+            reinterpret_cast<unsigned*>(ws)[i] = reinterpret_cast<const unsigned*>(&table)[i];
+    }
+    const int w = find_segment(table.sums_at, table.count, blockIdx.x), chunk = blockIdx.x - table.sums_at[w];
+    const void* const grad = table.grad[w];
+    float* const mem = table.mem[w];
+    const long long count = static_cast<long long>(table.s[w].n) * table.s[w].m, size = mu_chunk(count), first = chunk * size;
     const long long quads = min(count, first + size) / 4;
     double sum = 0.0;
 #pragma unroll 4
@@ -164,33 +167,37 @@ __global__ __launch_bounds__(256) void muon_moment(const Sources src, float beta
     sum = wave_sum(sum);
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) partial[src.partial[w] + chunk] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    if (threadIdx.x == 0) reinterpret_cast<double*>(ws + SUMS_AT)[blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 // X = u / |u| by rows and transposed, 64 x 64 entries a workgroup.  A matrix of zeros
 // stays zero; one with an entry that is not finite becomes NaN.
 template <bool BF16>
-__global__ __launch_bounds__(256) void muon_start(const Sources src, float beta, int nesterov, const double* partial, char* ws) {
+__global__ __launch_bounds__(256) void muon_start(const Table* __restrict__ table, float beta, int nesterov, char* ws) {
     __shared__ float tile[64][65];
     __shared__ double sums[4];
-    const int w = find_segment(src.begin, src.count, blockIdx.x), t = blockIdx.x - src.begin[w];
-    const int n = src.n[w], m = src.m[w], across = (m + 63) / 64;
+    const int w = find_segment(table->start_at, table->count, blockIdx.x), t = blockIdx.x - table->start_at[w];
+    const Shape s = table->s[w];
+    const bool turned = table->turned[w];
+    const int n = turned ? s.m : s.n, m = turned ? s.n : s.m, across = (m + 63) / 64;
     const int i0 = t / across * 64, j0 = t % across * 64;
-    const void* const grad = src.grad[w];
-    const float* const mem = src.mem[w];
-    float u[16];                                             // fetched while the norm is
+    const void* const grad = table->grad[w];
+    const float* const mem = table->mem[w];
+    // this thread's column of 16 rows, fetched together, and the partial sums
+    float u[16], v[16];
+    const int i1 = i0 + (threadIdx.x >> 6), j1 = j0 + (threadIdx.x & 63);
+    const long long last = static_cast<long long>(n) * m - 1;
+    auto place = [&](int p) { return min(static_cast<long long>(i1 + 4 * p) * m + j1, last); };
 #pragma unroll
-    for (int p = 0; p < 16; ++p) {
-        const int i = i0 + p * 4 + (threadIdx.x >> 6), j = j0 + (threadIdx.x & 63);
-        const bool in = i < n && j < m;
-        const long long at = in ? static_cast<long long>(i) * m + j : 0;
-        u[p] = load_grad1<BF16>(grad, at);
-        if (mem) u[p] = direction(mem[at], beta, u[p], nesterov);
-        if (!in) u[p] = 0.0f;
+    for (int p = 0; p < 16; ++p) u[p] = load_grad1<BF16>(grad, place(p));
+    if (mem) {
+#pragma unroll
+        for (int p = 0; p < 16; ++p) v[p] = mem[place(p)];
     }
     const int parts = mu_sums(static_cast<long long>(n) * m);
     double sum = 0.0;
-    for (int p = threadIdx.x; p < parts; p += 256) sum += partial[src.partial[w] + p];
+    const double* const partial = reinterpret_cast<const double*>(ws + SUMS_AT) + table->sums_at[w];
+    for (int p = threadIdx.x; p < parts; p += 256) sum += partial[p];
     sum = wave_sum(sum);
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
     __syncthreads();
@@ -198,12 +205,10 @@ __global__ __launch_bounds__(256) void muon_start(const Sources src, float beta,
     const double by = norm == 0.0 ? 0.0 : (norm < INFINITY ? SX / norm : static_cast<double>(NAN));
 #pragma unroll
     for (int p = 0; p < 16; ++p) {
-        const bool in = i0 + p * 4 + (threadIdx.x >> 6) < n && j0 + (threadIdx.x & 63) < m;
-        tile[p * 4 + (threadIdx.x >> 6)][threadIdx.x & 63] = in ? static_cast<float>(u[p] * by) : 0.0f;   // (by may be NaN)
+        const float x = mem ? direction(v[p], beta, u[p], nesterov) : u[p];
+        tile[p * 4 + (threadIdx.x >> 6)][threadIdx.x & 63] = i1 + 4 * p < n && j1 < m ? static_cast<float>(x * by) : 0.0f;   // (by may be NaN)
     }
     __syncthreads();
-    const bool turned = n > m;
-    const Shape s = {src.base[w], turned ? m : n, turned ? n : m};
     char* const by_rows = ws + (turned ? at_xt(s, 0) : at_x(s));
     char* const by_cols = ws + (turned ? at_x(s) : at_xt(s, 0));
 #pragma unroll
@@ -225,9 +230,6 @@ __global__ __launch_bounds__(256) void muon_start(const Sources src, float beta,
 
 // ---------------------------------------------------------------- products
 
-enum { GRAM, POLY, APPLY, LAST_F32, LAST_BF16 };
-constexpr bool symmetric(int kind) { return kind == GRAM || kind == POLY; }
-
 // The I-th row and J-th column of the t-th tile on or below the diagonal.
 __device__ __forceinline__ void below_diagonal(int t, int& I, int& J) {
     int i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
@@ -248,24 +250,25 @@ struct Job {
     unsigned pitch;
 };
 template <int KIND, int BM, int BN>
-__device__ __forceinline__ Job job_of(const Batch& batch, char* ws, int turn) {
+__device__ __forceinline__ Job job_of(const Table* __restrict__ table, char* ws, int turn) {
     Job b;
     const int block = static_cast<int>(xcd_place(blockIdx.x, gridDim.x));
-    b.w = find_segment(batch.begin, batch.count, block);
-    b.s = batch.s[b.w];
-    const int t = block - batch.begin[b.w];
+    const auto& at = table->tile_at[tile_kind(KIND)];
+    b.w = find_segment(at, table->count, block);
+    b.s = table->s[b.w];
+    const int t = block - at[b.w], per = KIND == GRAM ? table->per[b.w] : 0;
     int I, J, first = 0;
     b.part = -1;
     b.groups = static_cast<int>(mu_groups(KIND == GRAM ? b.s.m : b.s.n));
     b.pitch = static_cast<unsigned>(b.groups) * 128;
     if constexpr (symmetric(KIND)) {
         int tile = t;
-        if (KIND == GRAM && batch.per[b.w] < b.groups) {     // in parts
+        if (KIND == GRAM && per < b.groups) {     // in parts
             const int side = (b.s.n + BM - 1) / BM, tiles = side * (side + 1) / 2;
             b.part = t / tiles;
             tile = t - b.part * tiles;
-            first = b.part * batch.per[b.w];
-            b.groups = min(batch.per[b.w], b.groups - first);
+            first = b.part * per;
+            b.groups = min(per, b.groups - first);
         }
         below_diagonal(tile, I, J);
     } else {
@@ -294,14 +297,14 @@ __device__ __forceinline__ Job job_of(const Batch& batch, char* ws, int turn) {
 // columns a lane, and (for X, and for A and P off the diagonal) transposed, eight rows of a
 // column a lane, 32 rows one group.
 template <int KIND, int COLS>
-__device__ __forceinline__ void emit(float* region, const Job& b, int row0, int col0, const Ends& ends, char* ws, int turn, float ca,
+__device__ __forceinline__ void emit(float* region, const Job& b, int row0, int col0, const Table* __restrict__ table, char* ws, int turn, float ca,
                                      float cb, float cc) {
     constexpr bool LAST = KIND == LAST_F32 || KIND == LAST_BF16, BF16 = KIND == LAST_BF16;
     const Shape& s = b.s;
     const int lane = threadIdx.x & 63, rows = s.n, cols = symmetric(KIND) ? s.n : s.m;
     if (row0 >= rows || col0 >= cols) return;
-    const float by = KIND == GRAM ? (b.part < 0 ? SA / (SX * SX) : 1.0f) : KIND == APPLY ? 1.0f / SP : LAST ? ends.scale[b.w] / (SP * SX) : 1.0f;
-    const bool turned = LAST && ends.turned[b.w];
+    const float by = KIND == GRAM ? (b.part < 0 ? SA / (SX * SX) : 1.0f) : KIND == APPLY ? 1.0f / SP : LAST ? table->scale[b.w] / (SP * SX) : 1.0f;
+    const bool turned = LAST && table->turned[b.w];
     if (!turned) {
         constexpr int PER_ROW = COLS / 8;
         f16x8 old[KIND == POLY ? COLS / 16 : 1][2];          // of A, fetched together
@@ -336,11 +339,11 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
             if constexpr (LAST) {
                 const long long at = static_cast<long long>(row) * s.m + col;
                 if (col + 8 <= s.m) {
-                    store_out<BF16>(ends.out[b.w], at, v);
+                    store_out<BF16>(table->out[b.w], at, v);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        if (col + q < s.m) store1<BF16>(ends.out[b.w], at + q, v[q]);
+                        if (col + q < s.m) store1<BF16>(table->out[b.w], at + q, v[q]);
                 }
             } else {
                 if constexpr (KIND == POLY) {                // c A^2 + b A + a I, all times SP
@@ -370,11 +373,11 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
             if (col >= cols) continue;
             const long long at = static_cast<long long>(col) * s.n + row0 + k;
             if (row0 + k + 8 <= s.n) {
-                store_out<BF16>(ends.out[b.w], at, v);
+                store_out<BF16>(table->out[b.w], at, v);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    if (row0 + k + q < s.n) store1<BF16>(ends.out[b.w], at + q, v[q]);
+                    if (row0 + k + q < s.n) store1<BF16>(table->out[b.w], at + q, v[q]);
             }
         }
     } else {
@@ -410,8 +413,7 @@ __device__ __forceinline__ void lay(float* region, int y, const f32x16& acc) {
 // holds a row's 128 bytes together, its eight pieces permuted so that a fragment's reads
 // meet no bank twice: piece b of row i of a fragment at slot b ^ (i >> 1 & 7).
 template <int BM, int BN, int WM, int WN, int RING, int KIND, bool ONE>
-__global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Batch batch, const Ends ends, char* ws, int turn, float ca, float cb,
-                                                       float cc) {
+__global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict__ table, char* ws, int turn, float ca, float cb, float cc) {
     constexpr int NW = WM * WN, ROWS = BM + BN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr int CP = ROWS / 8 / NW;                       // 8-row copies a wave makes for a group
     constexpr int GROUP = ROWS * 128;
@@ -421,7 +423,7 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Batch batch, cons
     const unsigned lds_at = static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)lds));
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, i = lane & 31, wm = wave / WN, wn = wave % WN;
-    const Job b = job_of<KIND, BM, BN>(batch, ws, turn);
+    const Job b = job_of<KIND, BM, BN>(table, ws, turn);
     // a unit is what a place of the ring holds of a row: a group, or the hi halves of two
     const int groups = b.groups, units = ONE ? (groups + 1) / 2 : groups;
 
@@ -559,20 +561,20 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Batch batch, cons
             lay<COLS>(mine, y, acc[0][x][y]);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        emit<KIND, COLS>(mine, b, b.i0 + (wm * MI + x) * 32, b.j0 + wn * COLS, ends, ws, turn, ca, cb, cc);
+        emit<KIND, COLS>(mine, b, b.i0 + (wm * MI + x) * 32, b.j0 + wn * COLS, table, ws, turn, ca, cb, cc);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
 // A from the parts of its k, added in order: 64 x 64 entries on or below the diagonal.  On it
 // the entries above are those below (the parts may not have them).
-__global__ __launch_bounds__(256) void muon_join(const Batch batch, char* ws) {
+__global__ __launch_bounds__(256) void muon_join(const Table* __restrict__ table, char* ws) {
     __shared__ float sums[64][65];
-    const int w = find_segment(batch.begin, batch.count, blockIdx.x);
-    const Shape s = batch.s[w];
-    const int per = batch.per[w], parts = static_cast<int>((mu_groups(s.m) + per - 1) / per);
+    const int w = find_segment(table->join_at, table->count, blockIdx.x);
+    const Shape s = table->s[w];
+    const int per = table->per[w], parts = static_cast<int>((mu_groups(s.m) + per - 1) / per);
     int I, J;
-    below_diagonal(blockIdx.x - batch.begin[w], I, J);
+    below_diagonal(blockIdx.x - table->join_at[w], I, J);
     const int i0 = I * 64, j0 = J * 64;
     const long long ld = mu_groups(s.n) * 32, stride = s.n * ld, pitch = mu_groups(s.n) * 128;
     const float* const from = reinterpret_cast<const float*>(ws + at_parts(s));
@@ -696,14 +698,11 @@ Cut cut_of(const gc_muon_mat* mats, int count) {
     return cut;
 }
 
-// Workspace of up to MU_MAX matrices: partial sums, then each matrix's parts.
-int64_t layout(const gc_muon_mat* mats, int count, const Cut& cut, Shape* shapes, int* partial) {
+// Workspace of up to MU_MAX matrices: the table, partial sums, then each matrix's parts.
+int64_t layout(const gc_muon_mat* mats, int count, const Cut& cut, Shape* shapes) {
     int64_t sums = 0;
-    for (int w = 0; w < count; ++w) {
-        if (partial) partial[w] = static_cast<int>(sums);
-        sums += mu_sums(static_cast<int64_t>(mats[w].n) * mats[w].m);
-    }
-    int64_t at = static_cast<int64_t>(round_up(sums * 8, 1024));
+    for (int w = 0; w < count; ++w) sums += mu_sums(static_cast<int64_t>(mats[w].n) * mats[w].m);
+    int64_t at = SUMS_AT + static_cast<int64_t>(round_up(sums * 8, 1024));
     for (int w = 0; w < count; ++w) {
         Shape s = oriented(mats[w]);
         s.base = at;
@@ -718,7 +717,7 @@ int64_t workspace(const gc_muon_mat* mats, int nmats) {
     int64_t need = 0;
     for (int f = 0; f < nmats; f += MU_MAX) {
         const int count = std::min(MU_MAX, nmats - f);
-        need = std::max(need, layout(mats + f, count, cut_of(mats + f, count), nullptr, nullptr));
+        need = std::max(need, layout(mats + f, count, cut_of(mats + f, count), nullptr));
     }
     return need;
 }
@@ -751,16 +750,21 @@ bool coefs_ok(const float* coefs, int steps) {
     return true;
 }
 
-template <int KIND, bool ONE>
-void launch_product(Way way, Batch& batch, const Ends& ends, char* ws, int turn, const float* c, hipStream_t s) {
-    int64_t blocks = 0;
-    for (int w = 0; w < batch.count; ++w) {
-        batch.begin[w] = static_cast<int>(blocks);
-        blocks += blocks_of(KIND, way, batch.s[w], batch.per[w]);
+// Adds up workgroups: where each matrix's begin, and how many there are.
+template <typename F>
+unsigned place(int (&at)[MU_MAX], int count, F blocks) {
+    int64_t sum = 0;
+    for (int w = 0; w < count; ++w) {
+        at[w] = static_cast<int>(sum);
+        sum += blocks(w);
     }
-    const unsigned grid = static_cast<unsigned>(blocks);
+    return static_cast<unsigned>(sum);
+}
+
+template <int KIND, bool ONE>
+void launch_product(Way way, unsigned grid, char* ws, int turn, const float* c, hipStream_t s) {
     TimedLaunch tl("muon_tile", s);
-    auto go = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, s>>>(batch, ends, ws, turn, c[0], c[1], c[2]); };
+    auto go = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, s>>>(reinterpret_cast<const Table*>(ws), ws, turn, c[0], c[1], c[2]); };
     switch (way) {
         case TILE_64: go(muon_tile<64, 64, 2, 2, 4, KIND, ONE>, 256); break;
         case TILE_128: go(muon_tile<128, 128, 2, 4, 4, KIND, ONE>, 512); break;
@@ -771,74 +775,52 @@ void launch_product(Way way, Batch& batch, const Ends& ends, char* ws, int turn,
     }
 }
 
-// A of the matrices whose products are in parts.
-void launch_join(const Batch& all, char* ws, hipStream_t s) {
-    Batch batch;
-    batch.count = 0;
-    int64_t blocks = 0;
-    for (int w = 0; w < all.count; ++w) {
-        if (parts_of(all.s[w], all.per[w]) == 1) continue;
-        batch.s[batch.count] = all.s[w];
-        batch.per[batch.count] = all.per[w];
-        batch.begin[batch.count++] = static_cast<int>(blocks);
-        blocks += triangle(all.s[w].n, 64);
-    }
-    if (batch.count == 0) return;
-    TimedLaunch tl("muon_join", s);
-    muon_join<<<static_cast<unsigned>(blocks), 256, 0, s>>>(batch, ws);
-}
-
 int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float beta, int nesterov, int steps, const float* coefs,
         char* ws, hipStream_t s) {
     const Cut cut = cut_of(mats, count);
-    Sources src;
-    Batch batch;
-    Ends ends;
-    src.count = batch.count = count;
-    layout(mats, count, cut, batch.s, src.partial);
-    int64_t sums = 0, tiles = 0;
-    int begin[MU_MAX];
+    Table table;
+    table.count = count;
+    layout(mats, count, cut, table.s);
     for (int w = 0; w < count; ++w) {
         const gc_muon_mat& a = mats[w];
-        src.grad[w] = a.grad;
-        src.mem[w] = a.mem;
-        src.n[w] = a.n;
-        src.m[w] = a.m;
-        src.base[w] = batch.s[w].base;
-        src.begin[w] = static_cast<int>(sums);
-        sums += mu_sums(static_cast<int64_t>(a.n) * a.m);
-        begin[w] = static_cast<int>(tiles);
-        tiles += tiles_of(a.n, a.m, 64, 64);
-        batch.per[w] = cut.per[w];
-        ends.out[w] = a.out;
-        ends.scale[w] = a.scale;
-        ends.turned[w] = a.n > a.m;
+        table.grad[w] = a.grad;
+        table.mem[w] = a.mem;
+        table.out[w] = a.out;
+        table.per[w] = cut.per[w];
+        table.scale[w] = a.scale;
+        table.turned[w] = a.n > a.m;
     }
-    double* const partial = reinterpret_cast<double*>(ws);
+    const unsigned sums = place(table.sums_at, count, [&](int w) { return mu_sums(static_cast<int64_t>(mats[w].n) * mats[w].m); });
+    const unsigned tiles = place(table.start_at, count, [&](int w) { return tiles_of(mats[w].n, mats[w].m, 64, 64); });
+    const unsigned joins = place(table.join_at, count, [&](int w) { return parts_of(table.s[w], cut.per[w]) > 1 ? triangle(table.s[w].n, 64) : 0; });
+    unsigned grid[3];
+    for (int kind : {GRAM, POLY, APPLY})
+        grid[kind] = place(table.tile_at[kind], count, [&](int w) { return blocks_of(kind, cut.way[kind], table.s[w], cut.per[w]); });
+    const Table* const held = reinterpret_cast<const Table*>(ws);
     {
         TimedLaunch tl("muon_moment", s);
-        if (grad_dtype == GC_BF16) muon_moment<true><<<static_cast<unsigned>(sums), 256, 0, s>>>(src, beta, nesterov, partial);
-        else muon_moment<false><<<static_cast<unsigned>(sums), 256, 0, s>>>(src, beta, nesterov, partial);
+        if (grad_dtype == GC_BF16) muon_moment<true><<<sums, 256, 0, s>>>(table, beta, nesterov, ws);
+        else muon_moment<false><<<sums, 256, 0, s>>>(table, beta, nesterov, ws);
     }
-    int rc = check_launch("gc_muon_step");
-    if (rc != GC_OK) return rc;
-    std::copy(begin, begin + count, src.begin);
     {
         TimedLaunch tl("muon_start", s);
-        if (grad_dtype == GC_BF16) muon_start<true><<<static_cast<unsigned>(tiles), 256, 0, s>>>(src, beta, nesterov, partial, ws);
-        else muon_start<false><<<static_cast<unsigned>(tiles), 256, 0, s>>>(src, beta, nesterov, partial, ws);
+        if (grad_dtype == GC_BF16) muon_start<true><<<tiles, 256, 0, s>>>(held, beta, nesterov, ws);
+        else muon_start<false><<<tiles, 256, 0, s>>>(held, beta, nesterov, ws);
     }
-    rc = check_launch("gc_muon_step");
+    int rc = check_launch("gc_muon_step");
     for (int k = 0; k < steps && rc == GC_OK; ++k) {
         const float* c = coefs ? coefs + 3 * k : MU_COEFS;
         const bool last = k + 1 == steps, one = last && out_dtype == GC_BF16;
-        if (one) launch_product<GRAM, true>(cut.way[0], batch, ends, ws, k & 1, c, s);
-        else launch_product<GRAM, false>(cut.way[0], batch, ends, ws, k & 1, c, s);
-        launch_join(batch, ws, s);
-        launch_product<POLY, false>(cut.way[1], batch, ends, ws, k & 1, c, s);
-        if (!last) launch_product<APPLY, false>(cut.way[2], batch, ends, ws, k & 1, c, s);
-        else if (one) launch_product<LAST_BF16, true>(cut.way[2], batch, ends, ws, k & 1, c, s);
-        else launch_product<LAST_F32, false>(cut.way[2], batch, ends, ws, k & 1, c, s);
+        if (one) launch_product<GRAM, true>(cut.way[GRAM], grid[GRAM], ws, k & 1, c, s);
+        else launch_product<GRAM, false>(cut.way[GRAM], grid[GRAM], ws, k & 1, c, s);
+        if (joins > 0) {
+            TimedLaunch tl("muon_join", s);
+            muon_join<<<joins, 256, 0, s>>>(held, ws);
+        }
+        launch_product<POLY, false>(cut.way[POLY], grid[POLY], ws, k & 1, c, s);
+        if (!last) launch_product<APPLY, false>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
+        else if (one) launch_product<LAST_BF16, true>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
+        else launch_product<LAST_F32, false>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
         rc = check_launch("gc_muon_step");
     }
     return rc;
