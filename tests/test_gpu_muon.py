@@ -396,6 +396,75 @@ def test_training_steps_in_8_bits():
 
 # ---------------------------------------------------------------- large
 
+def one_step_on_device(u, coefs, bf16):
+    """one_step_bound in float64 on the device: (the step's result, what it may be off by)."""
+    x = u.double()
+    x = x / torch.linalg.vector_norm(x)
+    turned = x.shape[0] > x.shape[1]
+    x = x.t().contiguous() if turned else x
+    n, m = x.shape
+    a, b, c = (float(np.float32(v)) for v in coefs)
+    g = x @ x.t().contiguous()
+    p = b * g + c * (g @ g)
+    p.diagonal().add_(a)
+    want = p @ x
+    del g, p
+    ax = x.abs()
+    big = ax @ ax.t().contiguous()
+    square = big @ big
+    # the entries of `floors`, at most: every dX is 2^-37
+    dx = 2.0 ** -37
+    da = dx * (ax.sum(1)[:, None] + ax.sum(1)[None, :]) + 2.0 ** -36
+    dp = abs(b) * da + abs(c) * (big @ da + da @ big) + 2.0 ** -36
+    pa = abs(b) * big + abs(c) * square
+    e = 9 * 2.0 ** -22 + 3 * (m + 2 * n) * 2.0 ** -23
+    d = 9 * 2.0 ** -22 + (3 * n * 2.0 ** -23 if b or c else 0.0)
+    bound = 2 * (e * (pa @ ax) + d * abs(a) * ax + dx * (pa.sum(1, keepdim=True) + abs(a)) + dp @ ax)
+    if bf16:
+        bound += 2.0 ** -11 * 1.01 * (2 * abs(a) * ax + (4 * abs(b) * big + 6 * abs(c) * square) @ ax)
+    want, bound = (want.t(), bound.t()) if turned else (want, bound)
+    return want, bound * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs() if bf16 else bound
+
+
+# each tile for each product, whole k and parts of it, the last tile cut short, tall ones, sets of both
+LARGE = [[(1024, 1024)], [(1000, 4100)], [(700, 5000)], [(2048, 2048)], [(3500, 3000)], [(4097, 4000)], [(5000, 5003)], [(256, 30001)],
+         [(1024, 1000), (1024, 1024), (4096, 1024), (1000, 4096), (64, 64)], [(512, 520)] * 16, [(2001, 8000)]]
+
+
+@pytest.mark.parametrize("shapes", LARGE, ids=lambda s: "+".join(f"{n}x{m}" for n, m in dict.fromkeys(s)))
+def test_large_shapes(shapes):
+    gc = lib()
+    print(f"case: muon large {shapes}", flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(len(shapes) + shapes[0][0])
+    us = [torch.randn(s, generator=g, device=DEV) * torch.exp2(torch.randint(-3, 1, (s[0], 1), generator=g, device=DEV)) for s in shapes]
+    for coefs in (USUAL, (0.0, 1.0, 0.0)):
+        for dt in (torch.float32, torch.bfloat16):
+            outs = [torch.full((s[0] * s[1] + 8,), 7.0, dtype=dt, device=DEV) for s in shapes]
+            mats = gc.MuonArray([gc.MuonMat(u, o[:-8].view(u.shape)) for u, o in zip(us, outs)])
+            ws = workspace(mats)
+            gc.gc_muon_step(mats, 0.9, ws[: ws.numel() - 64], steps=1, coefs=coefs)
+            assert bool((ws[ws.numel() - 64:] == 255).all()) and all(bool((o[-8:] == 7.0).all()) for o in outs), "written past a buffer"
+            for u, o in zip(us[:1] + us[-3:], outs[:1] + outs[-3:]):
+                want, bound = one_step_on_device(u, coefs, dt == torch.bfloat16)
+                assert bool(((o[:-8].view(u.shape).double() - want).abs() <= bound).all())
+    # five steps, twice: the same bits, near the formula's in float32
+    outs = [[torch.empty_like(u) for u in us] for _ in range(2)]
+    for o in outs:
+        mats = gc.MuonArray([gc.MuonMat(u, t) for u, t in zip(us, o)])
+        gc.gc_muon_step(mats, 0.9, workspace(mats))
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
+    a, b, c = (float(np.float32(v)) for v in USUAL)
+    for u, o in zip(us[-1:], outs[0][-1:]):
+        x = (u.t().contiguous() if u.shape[0] > u.shape[1] else u).double()
+        x = x / torch.linalg.vector_norm(x)
+        for _ in range(5):
+            s = x @ x.t().contiguous()
+            x = a * x + (b * s + c * (s @ s)) @ x
+        x = x.t() if u.shape[0] > u.shape[1] else x
+        # what a step rounds, at most 8 * 2^-22 of X with independent roundings, grows four times in each that follows: 341 of them
+        assert float((o.double() - x).norm() / x.norm()) <= 341 * 8 * 2.0 ** -22
+
 def test_past_32_bits():
     """The largest square: parts of the workspace and of a held matrix past 2^32 bytes.  One step that gives X back."""
     gc = lib()
