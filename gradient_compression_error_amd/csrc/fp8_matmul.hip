@@ -201,8 +201,10 @@ __global__ __launch_bounds__(W * 64) void fp8_wave(const Operand A, const Operan
 // present one.
 //   256 x 256, four waves of 128 x 128, R = 2: every operand byte read from LDS serves
 //       128 rows, and a lane holds 256 accumulators.
-//   128 x 128, eight waves of 64 x 32, R = 4: a compute unit for each of up to 256 tiles.
-//   128 x 128, four waves of 64 x 64, R = 2: two tiles a compute unit for more than 256.
+//   128 x 128, four waves of 64 x 64, R = 4: a compute unit for each of up to 256 tiles.
+//   128 x 128, eight waves of 64 x 32, R = 4: the same where k is short and starting counts.
+//   128 x 128, four waves of 64 x 64, R = 2: two tiles a compute unit for more than 256, and
+//       all of EXACT, whose conversions want a second wave on each unit's vector pipe.
 //
 // A fragment is 32 rows of a stage; lane l takes row l % 32 and 32 bytes, the 16-byte
 // pieces 2 (l / 32) + 0, 1 of the stage's four.  LDS holds a row's 128 bytes of a group
@@ -247,23 +249,22 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
     constexpr int LATER = EARLY && R > 2 ? CP / 2 : 0, NOW = CP - LATER;
 
     // A lane's part of out, 16 bytes of PER_ROW lanes a row.  What is added to is fetched
-    // here, under the work, where a workgroup has a compute unit to itself and registers
-    // for it.
-    constexpr bool AHEAD = ADD && EARLY && R == 4;
+    // here, under the work, where there are registers for it (4096 x 1024 x 8192 to float32
+    // in 63 us, fetched at the end 67; alone 60), else all together when the work is done.
+    constexpr bool AHEAD = ADD && EARLY;
     constexpr int COLS = NI * 32, WIDE = BF16 ? 8 : 4, PER_ROW = COLS / WIDE, AT_ONCE = 64 / PER_ROW;
     const int col = j0 + wn * COLS + (lane % PER_ROW) * WIDE, row0 = i0 + wm * (BM / WM) + lane / PER_ROW;
     const int rows_left = A.rows - row0;                     // rows of this lane's from row0 on
     const bool whole = col + WIDE <= B.rows;                 // its 16 bytes are all there
-    u32x4_any old[AHEAD ? MI : 1][32 / AT_ONCE];
-    auto fetch = [&](int to, int x) {
+    u32x4_any old[MI][32 / AT_ONCE];
+    auto fetch = [&] {
 #pragma unroll
-        for (int t = 0; t < 32 / AT_ONCE; ++t)
-            if (whole && x * 32 + t * AT_ONCE < rows_left) old[to][t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
+        for (int x = 0; x < MI; ++x)
+#pragma unroll
+            for (int t = 0; t < 32 / AT_ONCE; ++t)
+                if (whole && x * 32 + t * AT_ONCE < rows_left) old[x][t] = load16<BF16>(out, (row0 + x * 32 + t * AT_ONCE) * ldo + col);
     };
-    if constexpr (AHEAD) {
-#pragma unroll
-        for (int x = 0; x < MI; ++x) fetch(x, x);
-    }
+    if constexpr (AHEAD) fetch();
 
     // Where this wave's copies come from: a uniform base per operand and a lane's
     // offset (below 2^32: a tile's rows are at most 256 times 2^24 bytes).  Rows
@@ -489,6 +490,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
     if (rest > 0) group(k0);
     if (rest > 1) group(k1);
     if (rest > 2) group(k2);
+    if constexpr (ADD && !AHEAD) fetch();
     wait_for<0>();
     meet();                                                  // every copy has landed, every fragment is read: LDS is free
 
@@ -500,7 +502,6 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
     float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * COLS;
 #pragma unroll
     for (int x = 0; x < MI; ++x) {
-        if constexpr (ADD && !AHEAD) fetch(0, x);
 #pragma unroll
         for (int y = 0; y < NI; ++y)
 #pragma unroll
@@ -523,7 +524,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile(const Operand A, const O
             }
             if (row >= A.rows) continue;
             if (whole) {
-                if constexpr (ADD) add16<BF16>(v, old[AHEAD ? x : 0][t]);
+                if constexpr (ADD) add16<BF16>(v, old[x][t]);
                 store16<BF16, OUT != OUT_PART>(out, row * ldo + col, v);
             } else {
                 put<BF16, ADD, WIDE>(out, row * ldo + col, v, B.rows - col);
@@ -542,7 +543,7 @@ __global__ __launch_bounds__(256) void fp8_join(const float* parts, int splits, 
 // ---------------------------------------------------------------- choice of the kernel
 
 struct Plan {
-    enum Kind { WAVE_1_1, WAVE_1_2, WAVE_2_1, WAVE_2_2, WAVE_2_4, WAVE_4_4, TILE_128, TILE_128_PAIRED, TILE_256 } kind;
+    enum Kind { WAVE_1_1, WAVE_1_2, WAVE_2_1, WAVE_2_2, WAVE_2_4, WAVE_4_4, TILE_128, TILE_128_SHORT, TILE_128_PAIRED, TILE_256 } kind;
     int splits, per_split;                                   // parts of k, groups of each
     int64_t ldp;                                             // entries between the rows of a part
 };
@@ -555,11 +556,12 @@ bool matmul_shape_ok(int64_t m, int64_t n, int64_t k) {
 // 8192 and k of 300 .. 16384, in graphs; a round is what 256 compute units take at once.
 // Both sides at some borders, bf16 out: 4 x 8192 x 8192 14.6 (1 x 1), 13.2 (1 x 2); 64 x 4096 x
 // 1024 5.6 (1 x 2), 4.9 (2 x 2), 5.8 (2 x 4); 777 x 1001 x 1155 10.0 (4 x 4), 8.4 (128); 1024 x
-// 1024 x 16384 47.9 (128), 27.3 (in four parts); 2048 x 4096 x 4096 37.1 (128), 34.2 (128, two a
+// 1024 x 16384 47.9 (128), 27.3 (in four parts); 1024 x 1024 x 1024 7.1 (128), 6.7 (128, short),
+// 2048 x 2048 x 2048 13.0 and 14.7; 2048 x 4096 x 4096 37.1 (128), 34.2 (128, two a
 // unit), 47.0 (256); 4096 x 4096 x 4096 68.1 (two a unit), 55.6 (256).  float32 out: 1024 x
-// 1024 x 1024 8.8 (4 x 4), 10.6 (128), 10.2 (two a unit, each alone); 4096 x 1024 x 8192 62.6 (128),
-// 58.6 (two a unit, each alone).  256 x 256 is not for float32, whose operands' wide forms
-// leave it no registers.
+// 1024 x 1024 8.8 (4 x 4), 10.2 (128); eight waves of 64 x 32 with four groups in flight took 5%
+// more than four of 64 x 64 with two (4096 x 1024 x 8192 62.6 and 58.6).  256 x 256 is not for
+// float32, whose operands' wide forms leave it no registers.
 Plan plan_of(int64_t m, int64_t n, int64_t k, bool exact) {
     const int groups = static_cast<int>(mx_groups(k));
     const double g = groups;
@@ -590,15 +592,14 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool exact) {
     const int64_t t128 = tiles_of(m, n, 128, 128), t256 = tiles_of(m, n, 256, 256);
     for (int s = 1; s <= MAX_SPLITS && t128 * s <= 256 && (s == 1 || groups >= 8 * s); s *= 2) {
         const double parts = s > 1 ? 3.0 + 0.35e-6 * 4.0 * s * static_cast<double>(m) * best.ldp : 0.0;
-        const double one = exact ? (t128 * s > 128 ? 0.88 : 0.67) : (t128 * s > 128 ? 0.42 : 0.34);
-        offer(Plan::TILE_128, (exact ? 5.5 : 4.8) + one * std::ceil(g / s) + parts, s);
+        const double mine = std::ceil(g / s), one = exact ? (t128 * s > 128 ? 0.83 : 0.68) : (t128 * s > 128 ? 0.42 : 0.34);
+        if (exact) offer(Plan::TILE_128_PAIRED, 5.2 + one * mine + parts, s);
+        else offer(mine <= 13 ? Plan::TILE_128_SHORT : Plan::TILE_128, 4.8 + one * mine + parts, s);
     }
     auto rounds = [](double x) { return x <= 1 ? 1.0 : (x + std::ceil(x)) / 2; };
     if (t128 > 256) {
         offer(Plan::TILE_128_PAIRED, rounds(t128 / 512.0) * (exact ? 5.0 + 1.58 * g : 4.5 + 0.95 * g), 1);
         if (!exact) offer(Plan::TILE_256, rounds(t256 / 256.0) * (8.0 + 1.48 * g), 1);
-    } else if (exact) {
-        offer(Plan::TILE_128_PAIRED, 5.2 + (t128 > 128 ? 0.83 : 0.68) * g, 1);
     }
     return best;
 }
@@ -621,7 +622,7 @@ void launch_tile(const Plan& p, const Operand& A, const Operand& B, int groups, 
         kernel<<<grid, WM * WN * 64, 0, s>>>(A, B, groups, sp, p.per_split, to, ld, stride);
     };
     if (p.splits > 1) {
-        if constexpr (BM == 128 && R == 4) go(fp8_tile<BM, BN, WM, WN, R, OUT_PART, EXACT>, ws, p.ldp, part * 4);   // only this one is split
+        if constexpr (BM == 128 && (R == 4 || EXACT)) go(fp8_tile<BM, BN, WM, WN, R, OUT_PART, EXACT>, ws, p.ldp, part * 4);   // only these are split
     } else if (add) {
         go(fp8_tile<BM, BN, WM, WN, R, EXACT ? OUT_F32_ADD : OUT_BF16_ADD, EXACT>, out, ldo, 0);
     } else {
@@ -686,10 +687,8 @@ int gc_fp8_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int a_block_r
         case Plan::WAVE_2_2: launch_wave<2, 2, 8, 4>(A, B, groups, sp, out, ldo, out_dtype, accumulate, s); break;
         case Plan::WAVE_2_4: launch_wave<2, 4, 8, 2>(A, B, groups, sp, out, ldo, out_dtype, accumulate, s); break;
         case Plan::WAVE_4_4: launch_wave<4, 4, 4, 2>(A, B, groups, sp, out, ldo, out_dtype, accumulate, s); break;
-        case Plan::TILE_128:
-            if (out_dtype == GC_BF16) launch_tile<128, 128, 2, 2, 4, false>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);
-            else launch_tile<128, 128, 2, 4, 4, true>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);
-            break;
+        case Plan::TILE_128: launch_tile<128, 128, 2, 2, 4, false>(p, A, B, groups, sp, out, ldo, accumulate, ws, s); break;
+        case Plan::TILE_128_SHORT: launch_tile<128, 128, 2, 4, 4, false>(p, A, B, groups, sp, out, ldo, accumulate, ws, s); break;
         case Plan::TILE_128_PAIRED:
             if (out_dtype == GC_BF16) launch_tile<128, 128, 2, 2, 2, false>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);
             else launch_tile<128, 128, 2, 2, 2, true>(p, A, B, groups, sp, out, ldo, accumulate, ws, s);

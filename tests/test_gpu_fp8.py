@@ -237,7 +237,8 @@ PRODUCTS = [(1, 1, 1), (1, 5, 33), (2, 16, 128), (1, 4096, 1024), (3, 1000, 2000
             (300, 520, 8192), (1000, 1155, 777), (512, 2048, 1024), (1024, 1024, 2048), (2049, 1025, 1030),
             (1, 20000, 300), (16, 9000, 1000), (30, 9000, 200), (777, 1001, 1155), (1100, 1500, 1500), (300, 520, 16384),
             (601, 1001, 16000), (2100, 2001, 100), (2100, 2001, 130), (2050, 2100, 700), (2100, 2000, 1000), (4000, 3970, 384),
-            (4001, 3900, 520), (3900, 4000, 1200), (3841, 4095, 1155), (2300, 2200, 4400)]
+            (4001, 3900, 520), (3900, 4000, 1200), (3841, 4095, 1155), (2300, 2200, 4400),
+            (9001, 10, 1000), (1100, 1500, 2000), (1001, 1901, 1900), (500, 1500, 500), (354, 1220, 100), (1050, 1030, 4300)]
 
 
 def exact_operands(m, n, k, ab, bb):
