@@ -539,6 +539,8 @@ size_t gc_muon_workspace_bytes(const gc_muon_mat* mats, int nmats);
  * apart.  For a bf16 out the last step, whose roundings nothing enlarges, takes
  * X X^T and the product with X from the 11-bit parts alone, and is off by 2e-4 to 8e-4
  * before the rounding to bf16, which is off by 1.7e-3.
+ * How sums are cut follows from the shapes of the whole set, so a matrix may have
+ * other last bits in another set.
  * Kernel launches only: no copy, no allocation, no synchronisation, so the call may
  * be captured in a HIP graph.  [host] arrays may be reused as soon as it returns.
  * Errors: GC_ERR_ARG (null or misaligned pointer, shape, steps or coefs out of
