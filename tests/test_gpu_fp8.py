@@ -101,6 +101,31 @@ def test_quantize_shapes(rows, cols, dtype, block):
     same(c2, by_cols)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols,pitch", [(8301, 700, 700), (8193, 1001, 1016), (4099, 1024, 1024), (1, 4300001, 4300001)])
+def test_quantize_large_rows(rows, cols, pitch, dtype):
+    """Where a thread takes two units at a time: the same bits as the matrix in pieces of few rows (or columns), with guards."""
+    gc = lib()
+    print(f"case: fp8 quantize large {rows}x{cols} pitch {pitch} {dtype}", flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(rows + cols)
+    x = torch.randn((rows, pitch), generator=g, device=DEV).to(dtype)[:, :cols]
+    r = Held(rows, cols)
+    gc.gc_fp8_quantize(x, *r.pair)
+    codes, scales = r.host()
+    codes, scales = codes.reshape(rows, -1), scales.reshape(rows, -1)
+    at = range(0, rows, 1500) if rows > 1 else range(0, cols, 512 * 2000)
+    for f in at:
+        piece = x[f:f + 1500] if rows > 1 else x[:, f:f + 512 * 2000].contiguous()
+        p = Held(*piece.shape)
+        gc.gc_fp8_quantize(piece, *p.pair)
+        c, s = (t.reshape(piece.shape[0], -1) for t in p.host())
+        if rows > 1:
+            assert np.array_equal(codes[f:f + 1500], c) and np.array_equal(scales[f:f + 1500], s)
+        else:
+            assert np.array_equal(codes[:, f:f + c.shape[1]], c) and np.array_equal(scales[:, f // 128:f // 128 + s.shape[1]], s)
+
+
 @pytest.mark.parametrize("block", [1, 128])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols,pitch", [(70, 129, 136), (70, 129, 131), (200, 512, 1024), (33, 64, 65), (1, 50, 99)])
