@@ -12,10 +12,7 @@
 // operands alone are 0.003 to 0.15 off in the end.  So X, A and P are held as pairs of f16,
 // hi = fl16(v 2^e), lo = fl16(v 2^e - hi), 22 to 24 bits together, and a product is three
 // matrix instructions, hi hi + hi lo + lo hi, summed in float32: as good as float32
-// products.  The last step's roundings are not enlarged: where the result is rounded to bf16
-// anyway, its A and its P X take the hi parts alone (ONE), which is 0.0002 to 0.0008 off, a
-// twentieth to a half of the rounding to bf16 (A A does not: the diagonal of A has entries
-// alike, whose roundings add up to 0.002).  The powers of two (SX, SA, SP) keep hi below f16's
+// products.  A bf16 result is the float32 one rounded once.  The powers of two (SX, SA, SP) keep hi below f16's
 // largest value, which the caller's coefficients are checked for, and lo above its least
 // for all but entries that do not matter; f16 subnormals are kept by the matrix instructions.
 //
@@ -419,7 +416,7 @@ __device__ __forceinline__ void lay(float* region, int y, const f32x16& acc) {
 // instructions work on the present one.  LDS
 // holds a row's 128 bytes together, its eight pieces permuted so that a fragment's reads
 // meet no bank twice: piece b of row i of a fragment at slot b ^ (i >> 1 & 7).
-template <int BM, int BN, int WM, int WN, int RING, int KIND, bool ONE>
+template <int BM, int BN, int WM, int WN, int RING, int KIND>
 __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict__ table, char* ws, int turn, float ca, float cb, float cc) {
     constexpr int NW = WM * WN, ROWS = BM + BN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr int CP = ROWS / 8 / NW;                       // 8-row copies a wave makes for a group
@@ -431,8 +428,7 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, i = lane & 31, wm = wave / WN, wn = wave % WN;
     const Job b = job_of<KIND, BM, BN>(table, ws, turn);
-    // a unit is what a place of the ring holds of a row: a group, or the hi halves of two
-    const int groups = b.groups, units = ONE ? (groups + 1) / 2 : groups;
+    const int groups = b.groups;
 
     // Where this wave's copies come from: rows past the end are the last one again (their
     // results are not written); 256 rows of 2^24 bytes stay within 32 bits.
@@ -441,18 +437,14 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
 #pragma unroll
     for (int c = 0; c < CP; ++c) {
         const int r = (c * NW + wave) * 8 + (lane >> 3);
-        off[c] = static_cast<unsigned>(c * 8 * NW < BM ? min(r, b.rows_l - 1) : min(r - BM, b.rows_r - 1)) * b.pitch + piece * 16 +
-                 (ONE && piece >= 4 ? 64 : 0);
+        off[c] = static_cast<unsigned>(c * 8 * NW < BM ? min(r, b.rows_l - 1) : min(r - BM, b.rows_r - 1)) * b.pitch + piece * 16;
     }
-    const unsigned second = ONE && piece >= 4 ? 128 : 0;     // what leads from the second group back to the first
-    auto copy = [&](int c, int unit, int place) {            // units past the end are the last again, a group past it the one before
-        const int u = min(unit, units - 1);
-        const unsigned back = ONE && 2 * u + 1 == groups ? second : 0;
-        copy16((c * 8 * NW < BM ? b.left : b.right) + u * (ONE ? 256ll : 128ll), off[c] - back, lds_at + place * GROUP + (c * NW + wave) * 1024);
+    auto copy = [&](int c, int group, int place) {           // groups past the end are the last again
+        copy16((c * 8 * NW < BM ? b.left : b.right) + min(group, groups - 1) * 128ll, off[c], lds_at + place * GROUP + (c * NW + wave) * 1024);
     };
 
     const int l_at = wm * MI * 4096 + i * 128, r_at = BM * 128 + wn * NI * 4096 + i * 128;
-    int c_at[2][2];                                          // byte of a row, by stage, hi and lo (or group)
+    int c_at[2][2];                                          // byte of a row, by stage, hi and lo
 #pragma unroll
     for (int q = 0; q < 4; ++q) c_at[q >> 1][q & 1] = (((q & 1) * 4 + 2 * (q >> 1) + half) ^ ((i >> 1) & 7)) * 16;
     auto read = [&](auto& l, auto& r, int place, int stage) {
@@ -471,7 +463,7 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
 
     // A matrix instruction waits for the one before on the same sums: with few fragments the
     // products hi hi, hi lo and lo hi have sums of their own.
-    constexpr int SETS = MI * NI < 4 ? (ONE ? 2 : 3) : 1;
+    constexpr int SETS = MI * NI < 4 ? 3 : 1;
     f32x16 acc[SETS][MI][NI];
 #pragma unroll
     for (int e = 0; e < SETS; ++e)
@@ -491,25 +483,25 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
     f16x8 l0[S][MI][2], r0[S][NI][2], l1[S][MI][2], r1[S][NI][2];
     read(l0, r0, 0, 0);
 
-    // Unit g + RING is copied in the last stage of unit g, into g's place, and has landed
-    // when its first fragments are read, in the last stage of unit g + RING - 1.
+    // Group g + RING is copied in the last stage of group g, into g's place, and has landed
+    // when its first fragments are read, in the last stage of group g + RING - 1.
     int g = 0, place = 0;
-    auto stage = [&](auto of_unit, auto products, auto& l, auto& r, auto& ln, auto& rn) {
-        constexpr int G = decltype(of_unit)::value, PRODUCTS = decltype(products)::value;
+    auto stage = [&](auto last_of_group, auto& l, auto& r, auto& ln, auto& rn) {
+        constexpr int G = decltype(last_of_group)::value;
         const int next = G ? (place == RING - 1 ? 0 : place + 1) : place;
         if constexpr (G == 1) {
-            wait_for<(RING - 2) * CP>();                     // the next unit has landed
+            wait_for<(RING - 2) * CP>();                     // the next group has landed
             wait_reads();                                    // and nobody reads this one any more
             meet();
             __builtin_amdgcn_sched_barrier(0);
         }
         read(ln, rn, next, S == 2 ? 0 : 1 - G);
         __builtin_amdgcn_sched_barrier(0);
-        constexpr int SLOTS = S * PRODUCTS * MI;
+        constexpr int SLOTS = S * 3 * MI;
 #pragma unroll
         for (int t = 0; t < SLOTS; ++t) {
-            // hi hi, then hi lo, then lo hi; or the hi hi of either group
-            const int x = t % MI, h = t / MI % PRODUCTS, k = t / MI / PRODUCTS, hl = ONE ? h : h == 2, hr = ONE ? h : h == 1;
+            // hi hi, then hi lo, then lo hi
+            const int x = t % MI, h = t / MI % 3, k = t / MI / 3, hl = h == 2, hr = h == 1;
 #pragma unroll
             for (int y = 0; y < NI; ++y) {
                 f32x16& sum = acc[SETS > 1 ? h : 0][x][y];
@@ -525,31 +517,18 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
     };
     constexpr std::integral_constant<int, 0> k0{};
     constexpr std::integral_constant<int, 1> k1{};
-    constexpr std::integral_constant<int, ONE ? 2 : 3> all{};
-    // (the last group of hi halves may have no second)
-    const int whole = ONE ? groups / 2 : groups;
     if constexpr (S == 1) {
-        for (; g < whole; ++g) {
-            stage(k0, all, l0, r0, l1, r1);
-            stage(k1, all, l1, r1, l0, r0);
-        }
-        if (ONE && g < units) {
-            stage(k0, k1, l0, r0, l1, r1);
-            stage(k1, k1, l1, r1, l0, r0);
+        for (; g < groups; ++g) {
+            stage(k0, l0, r0, l1, r1);
+            stage(k1, l1, r1, l0, r0);
         }
     } else {
-        for (; g + 1 < whole; ++g) {
-            stage(k1, all, l0, r0, l1, r1);
+        for (; g + 1 < groups; ++g) {
+            stage(k1, l0, r0, l1, r1);
             ++g;
-            stage(k1, all, l1, r1, l0, r0);
+            stage(k1, l1, r1, l0, r0);
         }
-        if (g < whole) {
-            stage(k1, all, l0, r0, l1, r1);
-            ++g;
-            if (ONE && g < units) stage(k1, k1, l1, r1, l0, r0);
-        } else if (ONE && g < units) {
-            stage(k1, k1, l0, r0, l1, r1);
-        }
+        if (g < groups) stage(k1, l0, r0, l1, r1);
     }
     wait_for<0>();
     wait_reads();
@@ -768,17 +747,17 @@ unsigned place(int (&at)[MU_MAX], int count, F blocks) {
     return static_cast<unsigned>(sum);
 }
 
-template <int KIND, bool ONE>
+template <int KIND>
 void launch_product(Way way, unsigned grid, char* ws, int turn, const float* c, hipStream_t s) {
     TimedLaunch tl("muon_tile", s);
     auto go = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, s>>>(reinterpret_cast<const Table*>(ws), ws, turn, c[0], c[1], c[2]); };
     switch (way) {
-        case TILE_64: go(muon_tile<64, 64, 2, 2, 4, KIND, ONE>, 256); break;
-        case TILE_128: go(muon_tile<128, 128, 2, 4, 4, KIND, ONE>, 512); break;
-        case TILE_128_PAIRED: go(muon_tile<128, 128, 2, 2, 2, KIND, ONE>, 256); break;
-        case TILE_192: go(muon_tile<192, 192, 2, 2, 3, KIND, ONE>, 256); break;
+        case TILE_64: go(muon_tile<64, 64, 2, 2, 4, KIND>, 256); break;
+        case TILE_128: go(muon_tile<128, 128, 2, 4, 4, KIND>, 512); break;
+        case TILE_128_PAIRED: go(muon_tile<128, 128, 2, 2, 2, KIND>, 256); break;
+        case TILE_192: go(muon_tile<192, 192, 2, 2, 3, KIND>, 256); break;
         default:
-            if constexpr (!symmetric(KIND)) go(muon_tile<256, 256, 2, 2, 2, KIND, ONE>, 256);
+            if constexpr (!symmetric(KIND)) go(muon_tile<256, 256, 2, 2, 2, KIND>, 256);
     }
 }
 
@@ -817,17 +796,15 @@ int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float
     int rc = check_launch("gc_muon_step");
     for (int k = 0; k < steps && rc == GC_OK; ++k) {
         const float* c = coefs ? coefs + 3 * k : MU_COEFS;
-        const bool last = k + 1 == steps, one = last && out_dtype == GC_BF16;
-        if (one) launch_product<GRAM, true>(cut.way[GRAM], grid[GRAM], ws, k & 1, c, s);
-        else launch_product<GRAM, false>(cut.way[GRAM], grid[GRAM], ws, k & 1, c, s);
+        launch_product<GRAM>(cut.way[GRAM], grid[GRAM], ws, k & 1, c, s);
         if (joins > 0) {
             TimedLaunch tl("muon_join", s);
             muon_join<<<joins, 256, 0, s>>>(held, ws);
         }
-        launch_product<POLY, false>(cut.way[POLY], grid[POLY], ws, k & 1, c, s);
-        if (!last) launch_product<APPLY, false>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
-        else if (one) launch_product<LAST_BF16, true>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
-        else launch_product<LAST_F32, false>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
+        launch_product<POLY>(cut.way[POLY], grid[POLY], ws, k & 1, c, s);
+        if (k + 1 < steps) launch_product<APPLY>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
+        else if (out_dtype == GC_BF16) launch_product<LAST_BF16>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
+        else launch_product<LAST_F32>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
         rc = check_launch("gc_muon_step");
     }
     return rc;

@@ -536,9 +536,7 @@ size_t gc_muon_workspace_bytes(const gc_muon_mat* mats, int nmats);
  * coefficients make what a step rounds up to 3.4 times as large with every step
  * that follows: a float32 out is within about 2e-4 of the exact one (2-norm over the
  * matrix's), and within 2e-6 to 2e-5 for matrices whose singular values are not far
- * apart.  For a bf16 out the last step, whose roundings nothing enlarges, takes
- * X X^T and the product with X from the 11-bit parts alone, and is off by 2e-4 to 8e-4
- * before the rounding to bf16, which is off by 1.7e-3.
+ * apart.  A bf16 out is the float32 one rounded once (1.7e-3).
  * How sums are cut follows from the shapes of the whole set, so a matrix may have
  * other last bits in another set.
  * Kernel launches only: no copy, no allocation, no synchronisation, so the call may
