@@ -12,9 +12,11 @@
 // operands alone are 0.003 to 0.15 off in the end.  So X, A and P are held as pairs of f16,
 // hi = fl16(v 2^e), lo = fl16(v 2^e - hi), 22 to 24 bits together, and a product is three
 // matrix instructions, hi hi + hi lo + lo hi, summed in float32: as good as float32
-// products.  A bf16 result is the float32 one rounded once.  The powers of two (SX, SA, SP) keep hi below f16's
-// largest value, which the caller's coefficients are checked for, and lo above its least
-// for all but entries that do not matter; f16 subnormals are kept by the matrix instructions.
+// products for entries that are not small.  A bf16 result is the float32 one rounded once.
+// f16 has a least value, 2^-24, and so have the pairs.  Each step's powers of two (Step) are the
+// largest that keep hi below f16's largest value: with the usual coefficients X and A are off by
+// 2^-40 at most however small an entry is, and P by 2^-39; float32 has no such limit.  f16 subnormals
+// are kept by the matrix instructions.
 //
 // Layout.  A held matrix has rows of groups of 32 columns, 128 bytes each: 32 hi, then
 // 32 lo, zeros behind the last column.  X is held by rows (for A) and transposed (for P X), A
@@ -41,7 +43,6 @@ constexpr int MU_SUMS = 1024;          // partial sums of squares of a matrix, a
 constexpr int64_t MU_MAX_SIDE = int64_t(1) << 22;
 constexpr int MU_MAX_STEPS = 32;
 constexpr int MU_MAX_PARTS = 64;
-constexpr float SX = 4096.0f, SA = 2048.0f, SP = 2048.0f;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -68,6 +69,11 @@ __host__ __device__ inline int mu_chunk(long long entries) {
     return static_cast<int>(even <= 2048 ? 2048 : (even + 1023) / 1024 * 1024);
 }
 __host__ __device__ inline int mu_sums(long long entries) { return static_cast<int>((entries + mu_chunk(entries) - 1) / mu_chunk(entries)); }
+
+// What a product's sums are multiplied by; for P also what A is, and what its diagonal gets.
+struct Factors {
+    float out, old, one;
+};
 
 enum { GRAM, POLY, APPLY, LAST_F32, LAST_BF16 };
 constexpr bool symmetric(int kind) { return kind == GRAM || kind == POLY; }
@@ -173,11 +179,11 @@ __global__ __launch_bounds__(256) void muon_moment(const Table table, float beta
     if (threadIdx.x == 0) reinterpret_cast<double*>(ws + SUMS_AT)[blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
-// X = u / |u| by rows and transposed, 64 x 64 entries a workgroup.  A matrix of zeros
+// X = u / |u| (times sx) by rows and transposed, 64 x 64 entries a workgroup.  A matrix of zeros
 // stays zero; one with an entry that is not finite becomes NaN.  Bound by HBM: 12.6M float32
 // entries in 39 us (16 bytes each, 5.1 TB/s), the norm needed before any of it.
 template <bool BF16>
-__global__ __launch_bounds__(256) void muon_start(const Table* __restrict__ table, float beta, int nesterov, char* ws) {
+__global__ __launch_bounds__(256) void muon_start(const Table* __restrict__ table, float beta, int nesterov, float sx, char* ws) {
     __shared__ float tile[64][65];
     __shared__ double sums[4];
     const int w = find_segment(table->start_at, table->count, blockIdx.x), t = blockIdx.x - table->start_at[w];
@@ -206,7 +212,7 @@ __global__ __launch_bounds__(256) void muon_start(const Table* __restrict__ tabl
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
     __syncthreads();
     const double norm = sqrt((sums[0] + sums[1]) + (sums[2] + sums[3]));
-    const double by = norm == 0.0 ? 0.0 : (norm < INFINITY ? SX / norm : static_cast<double>(NAN));
+    const double by = norm == 0.0 ? 0.0 : (norm < INFINITY ? sx / norm : static_cast<double>(NAN));
 #pragma unroll
     for (int p = 0; p < 16; ++p) {
         const float x = mem ? direction(v[p], beta, u[p], nesterov) : u[p];
@@ -301,13 +307,13 @@ __device__ __forceinline__ Job job_of(const Table* __restrict__ table, char* ws,
 // columns a lane, and (for X, and for A and P off the diagonal) transposed, eight rows of a
 // column a lane, 32 rows one group.
 template <int KIND, int COLS>
-__device__ __forceinline__ void emit(float* region, const Job& b, int row0, int col0, const Table* __restrict__ table, char* ws, int turn, float ca,
-                                     float cb, float cc) {
+__device__ __forceinline__ void emit(float* region, const Job& b, int row0, int col0, const Table* __restrict__ table, char* ws, int turn,
+                                     const Factors& f) {
     constexpr bool LAST = KIND == LAST_F32 || KIND == LAST_BF16, BF16 = KIND == LAST_BF16;
     const Shape& s = b.s;
     const int lane = threadIdx.x & 63, rows = s.n, cols = symmetric(KIND) ? s.n : s.m;
     if (row0 >= rows || col0 >= cols) return;
-    const float by = KIND == GRAM ? (b.part < 0 ? SA / (SX * SX) : 1.0f) : KIND == APPLY ? 1.0f / SP : LAST ? table->scale[b.w] / (SP * SX) : 1.0f;
+    const float by = KIND == GRAM && b.part >= 0 ? 1.0f : LAST ? table->scale[b.w] * f.out : f.out;
     const bool turned = LAST && table->turned[b.w];
     if (!turned) {
         constexpr int PER_ROW = COLS / 8;
@@ -327,8 +333,8 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
             float v[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float4 f = *reinterpret_cast<const float4*>(region + r * COLS + ((c / 4 + q) ^ (r & 7)) * 4);
-                v[4 * q] = by * f.x; v[4 * q + 1] = by * f.y; v[4 * q + 2] = by * f.z; v[4 * q + 3] = by * f.w;
+                const float4 sum = *reinterpret_cast<const float4*>(region + r * COLS + ((c / 4 + q) ^ (r & 7)) * 4);
+                v[4 * q] = by * sum.x; v[4 * q + 1] = by * sum.y; v[4 * q + 2] = by * sum.z; v[4 * q + 3] = by * sum.w;
             }
             if (row >= rows) continue;
             if (KIND == GRAM && b.part >= 0) {
@@ -350,11 +356,11 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
                         if (col + q < s.m) store1<BF16>(table->out[b.w], at + q, v[q]);
                 }
             } else {
-                if constexpr (KIND == POLY) {                // c A^2 + b A + a I, all times SP
+                if constexpr (KIND == POLY) {                // c A^2 + b A + a I
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        v[q] = cc * (SP / (SA * SA)) * v[q] + cb * (SP / SA) * (static_cast<float>(old[p][0][q]) + static_cast<float>(old[p][1][q]));
-                        if (row == col + q) v[q] += ca * SP;
+                        v[q] += f.old * (static_cast<float>(old[p][0][q]) + static_cast<float>(old[p][1][q]));
+                        if (row == col + q) v[q] += f.one;
                     }
 #pragma unroll
                     for (int q = 0; q < 2; ++q)              // for the transposed form
@@ -417,7 +423,7 @@ __device__ __forceinline__ void lay(float* region, int y, const f32x16& acc) {
 // holds a row's 128 bytes together, its eight pieces permuted so that a fragment's reads
 // meet no bank twice: piece b of row i of a fragment at slot b ^ (i >> 1 & 7).
 template <int BM, int BN, int WM, int WN, int RING, int KIND>
-__global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict__ table, char* ws, int turn, float ca, float cb, float cc) {
+__global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict__ table, char* ws, int turn, Factors f) {
     constexpr int NW = WM * WN, ROWS = BM + BN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr int CP = ROWS / 8 / NW;                       // 8-row copies a wave makes for a group
     constexpr int GROUP = ROWS * 128;
@@ -547,14 +553,14 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
             lay<COLS>(mine, y, acc[0][x][y]);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        emit<KIND, COLS>(mine, b, b.i0 + (wm * MI + x) * 32, b.j0 + wn * COLS, table, ws, turn, ca, cb, cc);
+        emit<KIND, COLS>(mine, b, b.i0 + (wm * MI + x) * 32, b.j0 + wn * COLS, table, ws, turn, f);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
 // A from the parts of its k, added in order: 64 x 64 entries on or below the diagonal.  On it
 // the entries above are those below (the parts may not have them).
-__global__ __launch_bounds__(256) void muon_join(const Table* __restrict__ table, char* ws) {
+__global__ __launch_bounds__(256) void muon_join(const Table* __restrict__ table, char* ws, float by) {
     __shared__ float sums[64][65];
     const int w = find_segment(table->join_at, table->count, blockIdx.x);
     const Shape s = table->s[w];
@@ -579,7 +585,7 @@ __global__ __launch_bounds__(256) void muon_join(const Table* __restrict__ table
             }
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sums[r][c + q] = v[q] * (SA / (SX * SX));
+        for (int q = 0; q < 8; ++q) sums[r][c + q] = v[q] * by;
     }
     __syncthreads();
 #pragma unroll
@@ -710,12 +716,23 @@ int64_t workspace(const gc_muon_mat* mats, int nmats) {
 
 const float MU_COEFS[3] = {3.4445f, -4.7750f, 2.0315f};
 
-// Whether X, A and P stay in the range that their pairs hold: with singular values up to
-// `top`, the polynomial's largest value over them at each step, and P's.
-bool coefs_ok(const float* coefs, int steps) {
+// A step's coefficients, and the powers of two that it holds X (which it starts from), A and P times.
+struct Step {
+    float a, b, c, sx, sa, sp;
+};
+
+// The largest power of two, 2^30 at most, that keeps values of up to `most` in f16's range, with
+// a tenth of it left for roundings, which the bounds below do not know.
+float power_for(double most) { return std::ldexp(1.0f, std::min(30, std::ilogb(59000.0 / std::max(most, 1e-6)))); }
+
+// The steps of a call, and one more for the X of its result.  With singular values up to `top` at each
+// step, the polynomial's largest value over them and P's say what X, A and P may reach: false
+// where that leaves the range that pairs are good for.
+bool steps_of(const float* coefs, int steps, Step* to) {
     double top = 1.0;
     for (int k = 0; k < steps; ++k) {
-        const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2], t1 = top * top;
+        const float* const f = coefs ? coefs + 3 * k : MU_COEFS;
+        const double a = f[0], b = f[1], c = f[2], t1 = top * top;
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
         double p = std::max(std::abs(a), std::abs(a + b * t1 + c * t1 * t1)), x = std::abs((a + b * t1 + c * t1 * t1) * top);
         auto value = [&](double t) {
@@ -731,8 +748,10 @@ bool coefs_ok(const float* coefs, int steps) {
             value(-a / (3 * b));
         }
         if (p > 16.0 || x > 4.0) return false;
+        to[k] = {f[0], f[1], f[2], power_for(top), power_for(t1), power_for(p)};
         top = x;
     }
+    to[steps].sx = power_for(top);
     return true;
 }
 
@@ -748,9 +767,9 @@ unsigned place(int (&at)[MU_MAX], int count, F blocks) {
 }
 
 template <int KIND>
-void launch_product(Way way, unsigned grid, char* ws, int turn, const float* c, hipStream_t s) {
+void launch_product(Way way, unsigned grid, char* ws, int turn, const Factors& f, hipStream_t s) {
     TimedLaunch tl("muon_tile", s);
-    auto go = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, s>>>(reinterpret_cast<const Table*>(ws), ws, turn, c[0], c[1], c[2]); };
+    auto go = [&](auto kernel, int threads) { kernel<<<grid, threads, 0, s>>>(reinterpret_cast<const Table*>(ws), ws, turn, f); };
     switch (way) {
         case TILE_64: go(muon_tile<64, 64, 2, 2, 4, KIND>, 256); break;
         case TILE_128: go(muon_tile<128, 128, 2, 4, 4, KIND>, 512); break;
@@ -761,7 +780,7 @@ void launch_product(Way way, unsigned grid, char* ws, int turn, const float* c, 
     }
 }
 
-int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float beta, int nesterov, int steps, const float* coefs,
+int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float beta, int nesterov, int steps, const Step* step,
         char* ws, hipStream_t s) {
     const Cut cut = cut_of(mats, count);
     Table table;
@@ -790,21 +809,24 @@ int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float
     }
     {
         TimedLaunch tl("muon_start", s);
-        if (grad_dtype == GC_BF16) muon_start<true><<<tiles, 256, 0, s>>>(held, beta, nesterov, ws);
-        else muon_start<false><<<tiles, 256, 0, s>>>(held, beta, nesterov, ws);
+        if (grad_dtype == GC_BF16) muon_start<true><<<tiles, 256, 0, s>>>(held, beta, nesterov, step[0].sx, ws);
+        else muon_start<false><<<tiles, 256, 0, s>>>(held, beta, nesterov, step[0].sx, ws);
     }
     int rc = check_launch("gc_muon_step");
     for (int k = 0; k < steps && rc == GC_OK; ++k) {
-        const float* c = coefs ? coefs + 3 * k : MU_COEFS;
-        launch_product<GRAM>(cut.way[GRAM], grid[GRAM], ws, k & 1, c, s);
+        const Step& t = step[k];
+        const bool last = k + 1 == steps;
+        const Factors gram = {t.sa / (t.sx * t.sx), 0, 0}, poly = {t.c * (t.sp / (t.sa * t.sa)), t.b * (t.sp / t.sa), t.a * t.sp},
+                      apply = {(last ? 1.0f : step[k + 1].sx) / (t.sp * t.sx), 0, 0};
+        launch_product<GRAM>(cut.way[GRAM], grid[GRAM], ws, k & 1, gram, s);
         if (joins > 0) {
             TimedLaunch tl("muon_join", s);
-            muon_join<<<joins, 256, 0, s>>>(held, ws);
+            muon_join<<<joins, 256, 0, s>>>(held, ws, gram.out);
         }
-        launch_product<POLY>(cut.way[POLY], grid[POLY], ws, k & 1, c, s);
-        if (k + 1 < steps) launch_product<APPLY>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
-        else if (out_dtype == GC_BF16) launch_product<LAST_BF16>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
-        else launch_product<LAST_F32>(cut.way[APPLY], grid[APPLY], ws, k & 1, c, s);
+        launch_product<POLY>(cut.way[POLY], grid[POLY], ws, k & 1, poly, s);
+        if (!last) launch_product<APPLY>(cut.way[APPLY], grid[APPLY], ws, k & 1, apply, s);
+        else if (out_dtype == GC_BF16) launch_product<LAST_BF16>(cut.way[APPLY], grid[APPLY], ws, k & 1, apply, s);
+        else launch_product<LAST_F32>(cut.way[APPLY], grid[APPLY], ws, k & 1, apply, s);
         rc = check_launch("gc_muon_step");
     }
     return rc;
@@ -830,7 +852,8 @@ int gc_muon_step(const gc_muon_mat* mats, int nmats, int grad_dtype, int out_dty
     if (grad_dtype != GC_F32 && grad_dtype != GC_BF16) return fail(GC_ERR_DTYPE, "gc_muon_step: grad_dtype must be GC_F32 or GC_BF16");
     if (out_dtype != GC_F32 && out_dtype != GC_BF16) return fail(GC_ERR_DTYPE, "gc_muon_step: out_dtype must be GC_F32 or GC_BF16");
     if (steps < 1 || steps > MU_MAX_STEPS) return fail(GC_ERR_ARG, "gc_muon_step: steps must be in [1, 32]");
-    if (coefs && !coefs_ok(coefs, steps))
+    Step step[MU_MAX_STEPS + 1];
+    if (!steps_of(coefs, steps, step))
         return fail(GC_ERR_ARG, "gc_muon_step: coefficients that take singular values past 4, or the factor of a step past 16");
     for (int w = 0; w < nmats; ++w) {
         const gc_muon_mat& a = mats[w];
@@ -867,7 +890,7 @@ int gc_muon_step(const gc_muon_mat* mats, int nmats, int grad_dtype, int out_dty
         if (sp.written) written_end = std::max(written_end, sp.to);
     }
     for (int f = 0; f < nmats; f += MU_MAX) {
-        const int rc = run(mats + f, std::min(MU_MAX, nmats - f), grad_dtype, out_dtype, beta, nesterov != 0, steps, coefs,
+        const int rc = run(mats + f, std::min(MU_MAX, nmats - f), grad_dtype, out_dtype, beta, nesterov != 0, steps, step,
                            static_cast<char*>(ws), static_cast<hipStream_t>(stream));
         if (rc != GC_OK) return rc;
     }

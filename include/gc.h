@@ -531,12 +531,18 @@ size_t gc_muon_workspace_bytes(const gc_muon_mat* mats, int nmats);
  *            [0, 1], may not pass 4, nor may |a + b s^2 + c s^4| pass 16.
  *   ws       >= gc_muon_workspace_bytes(mats, nmats) bytes
  * Sums are in float32 (the norm's in float64); X, A and a + b A + c A A are held as
- * pairs of 11-bit floating point numbers, 22 to 24 bits together and nothing below
- * 2^-37 (X's entries are at most 4), and rounded once to out.  The usual
- * coefficients make what a step rounds up to 3.4 times as large with every step
+ * pairs of 11-bit floating point numbers, 22 to 24 bits together, and rounded once to
+ * out.  The usual coefficients make what a step rounds up to 3.4 times as large with every step
  * that follows: a float32 out is within about 2e-4 of the exact one (2-norm over the
  * matrix's), and within 2e-6 to 2e-5 for matrices whose singular values are not far
  * apart.  A bf16 out is the float32 one rounded once (1.7e-3).
+ *   Pairs have a least value, which float32 has not: with the usual coefficients an entry
+ * of X (the whole of which has norm 1 at first) or A is off by up to 2^-40 however
+ * small it is, one of a + b A + c A A by 2^-39 (by up to 2^-38, 2^-36 and 2^-36 with others).
+ * The matrix as a whole does not notice, but rows or columns much smaller than the
+ * rest do: at 2^-12 of the others' size they are about as good as float32's, at 2^-16
+ * they are off by 5e-6 (64 x 576) to 3e-5 (1024 x 1024) of their own size, at 2^-20 by 8e-5
+ * to 4e-4, at 2^-24 by 1e-3 to 7e-3.
  * How sums are cut follows from the shapes of the whole set, so a matrix may have
  * other last bits in another set.
  * Kernel launches only: no copy, no allocation, no synchronisation, so the call may

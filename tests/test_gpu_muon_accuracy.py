@@ -3,8 +3,9 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_util import DEV, require_gpu
-from test_gpu_muon import matrix, step
+import oracle
+from gpu_util import require_gpu
+from test_gpu_muon import USUAL, matrix, step
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +29,38 @@ def test_bf16_is_the_float32_result_rounded_once(shapes, steps):
     got, _ = step(grads, steps=steps, out_dtype=torch.bfloat16)
     for w, g in zip(exact, got):
         assert torch.equal(g, w.to(torch.bfloat16))
+
+
+def least(x, b, c, dx, da, dp):
+    """What held values' least value puts on one step's result, entry by entry: X off by dx, A by da and P by dp at most."""
+    big = np.abs(x) @ np.abs(x).T
+    p = b * big + c * (big @ big)
+    off_a = dx * (np.abs(x).sum(1)[:, None] + np.abs(x).sum(1)[None, :]) + da
+    off_p = b * off_a + c * (big @ off_a + off_a @ big) + dp
+    return dx * p.sum(1, keepdims=True) + off_p @ np.abs(x), p
+
+
+@pytest.mark.parametrize("down", [-12, -20, -24])
+@pytest.mark.parametrize("axis", [0, 1])
+@pytest.mark.parametrize("n,m", [(64, 576), (576, 64), (33, 31), (130, 257), (300, 1111)])
+def test_parts_much_smaller_than_the_rest(n, m, axis, down):
+    """Half of the rows, or of the columns, `down` binades below the others: one step, entry by entry.  The bound is
+    test_gpu_muon's with what the pairs cannot hold at the powers of two that a step of singular values up to 1 has: X and
+    A 2^15 and P 2^14 times themselves, each off by half of f16's least value, 2^-25."""
+    print(f"case: muon {n}x{m}, parts 2^{down} along {axis}", flush=True)
+    u = matrix(n, m, "gauss", 41)
+    small = np.exp2(down).astype(np.float32)
+    (u if axis == 0 else u.T)[::2] *= small
+    x = u.astype(np.float64) / np.linalg.norm(u.astype(np.float64))
+    x = x.T if n > m else x
+    k, w = x.shape
+    a, b, c = (abs(float(np.float32(v))) for v in USUAL)
+    floor, p = least(x, b, c, 2.0 ** -40, 2.0 ** -40, 2.0 ** -39)
+    e = 9 * 2.0 ** -22 + 3 * (w + 2 * k) * 2.0 ** -23
+    d = 9 * 2.0 ** -22 + 3 * k * 2.0 ** -23
+    bound = 2 * (e * (p @ np.abs(x)) + d * a * np.abs(x) + floor + a * 2.0 ** -40)
+    want = oracle.newton_schulz(u, 1)
+    want = want.T if n > m else want
+    (got,), _ = step([u], steps=1)
+    got = got.double().numpy()
+    assert np.all(np.abs((got.T if n > m else got) - want) <= bound)
