@@ -313,7 +313,8 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
     const Shape& s = b.s;
     const int lane = threadIdx.x & 63, rows = s.n, cols = symmetric(KIND) ? s.n : s.m;
     if (row0 >= rows || col0 >= cols) return;
-    const float by = KIND == GRAM && b.part >= 0 ? 1.0f : LAST ? table->scale[b.w] * f.out : f.out;
+    const float by = KIND == GRAM && b.part >= 0 ? 1.0f : f.out;
+    const float scale = LAST ? table->scale[b.w] : 1.0f;     // (not into `by`, which a small one would take below 2^-126)
     const bool turned = LAST && table->turned[b.w];
     if (!turned) {
         constexpr int PER_ROW = COLS / 8;
@@ -348,6 +349,8 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
             }
             if constexpr (LAST) {
                 const long long at = static_cast<long long>(row) * s.m + col;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] *= scale;
                 if (col + 8 <= s.m) {
                     store_out<BF16>(table->out[b.w], at, v);
                 } else {
@@ -379,7 +382,7 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
             const int c = p * 16 + (lane >> 2), k = (lane & 3) * 8, col = col0 + c;
             float v[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = by * region[(k + q) * COLS + ((c >> 2) ^ (k + q & 7)) * 4 + (c & 3)];
+            for (int q = 0; q < 8; ++q) v[q] = scale * (by * region[(k + q) * COLS + ((c >> 2) ^ (k + q & 7)) * 4 + (c & 3)]);
             if (col >= cols) continue;
             const long long at = static_cast<long long>(col) * s.n + row0 + k;
             if (row0 + k + 8 <= s.n) {

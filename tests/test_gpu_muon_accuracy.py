@@ -64,3 +64,18 @@ def test_parts_much_smaller_than_the_rest(n, m, axis, down):
     (got,), _ = step([u], steps=1)
     got = got.double().numpy()
     assert np.all(np.abs((got.T if n > m else got) - want) <= bound)
+
+
+@pytest.mark.parametrize("n,m", [(33, 50), (50, 33)])
+def test_small_and_large_scales(n, m):
+    """A scale is one rounding of each entry, 2^-24 of it, as far as the results are normal."""
+    print(f"case: muon {n}x{m}, scales near float32's ends", flush=True)
+    u = matrix(n, m, "gauss", 42)
+    (one,), _ = step([u])
+    one = one.double().numpy()
+    for scale in (1.1e-36, -3.3e-33, 1.7e38):
+        (got,), _ = step([u], scales=[scale])
+        want = one * float(np.float32(scale))
+        normal = np.abs(want) >= 2.0 ** -126
+        assert normal.mean() > 0.5
+        assert np.all(np.abs(got.double().numpy() - want)[normal] <= 2.0 ** -24 * np.abs(want)[normal])
