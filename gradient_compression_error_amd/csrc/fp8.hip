@@ -6,9 +6,10 @@
 // largest magnitude and f its fraction in [1, 2):
 //     s = max(E - 8 + (f > 1.75), 0)
 //     code = RNE_E4M3(x * 2^(127 - s))
-// so the largest entry lands in (224, 448] and nothing saturates.  A power of two costs no
-// bit of the codes' significands, and the matrix instructions take it as an operand.  A
-// block with an entry that is not finite gets s = 255 (NaN) and zero codes.
+// so the largest entry lands in (224, 448] and nothing saturates, but for float32's last half
+// step: what would round to 2^128 (256 at s = 247) becomes 240, so that finite entries stay finite.
+// A power of two costs no bit of the codes' significands, and the matrix instructions take it as
+// an operand.  A block with an entry that is not finite gets s = 255 (NaN) and zero codes.
 //
 // All of it is bound by HBM traffic (3 to 6 bytes an entry and form), small calls by the
 // launch.
@@ -63,11 +64,15 @@ struct Eight<false> : Entries8<false> {
     }
 };
 
+// Four codes at s = 247, where 256 (magnitude 0x78, the largest that occurs) would be 2^128.
+__device__ __forceinline__ unsigned below_2_128(unsigned c) { return c - ((c >> 3) & (c >> 4) & (c >> 5) & (c >> 6) & 0x01010101u); }
+
 // Eight entries' codes; zeros where the block is not finite.
 template <bool BF16>
 __device__ __forceinline__ uint2 codes_of(const Eight<BF16>& e, unsigned s) {
     const float scale = scale_operand(s);
-    const unsigned a = e.four(0, scale), b = e.four(1, scale);
+    unsigned a = e.four(0, scale), b = e.four(1, scale);
+    if (s == 247u) a = below_2_128(a), b = below_2_128(b);
     return s == 255u ? make_uint2(0, 0) : make_uint2(a, b);
 }
 

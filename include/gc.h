@@ -432,7 +432,9 @@ int gc_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const uint8
  * Quantising a block (Q8 below): the scale is the least power of two, 2^-127 at
  * least, that takes the block's largest magnitude to at most 448; a code is
  * entry / scale rounded to the nearest E4M3 value (ties to the even code), with
- * the entry's sign.  Nothing saturates.  A block with an entry that is not
+ * the entry's sign.  Nothing saturates, except that an entry which would round to
+ * 2^128 (of magnitude 1.9375 * 2^127 and more) becomes the value below it, 1.875 *
+ * 2^127: finite entries have finite values.  A block with an entry that is not
  * finite gets s = 255 and zero codes.  D8 gives back the values, exactly, in
  * float32 (a value past its range, from bytes that no call here writes, is
  * infinite). */

@@ -10,6 +10,7 @@ Readings taken:
     block of zeros has the least scale; a block with an entry that is not finite
     has the NaN scale (byte 255) and zero codes;
   * codes round to nearest, ties to the even code, and keep the entry's sign;
+    what would so become 2^128, past float32's range, is the value below it;
   * rows are held in groups of 128 columns, pads are zero codes; a row of blocks
     has its scale bytes padded with zeros to a multiple of four.
 """
@@ -60,7 +61,8 @@ def fp8_quantize(x: np.ndarray, block_rows: int = 1):
     scales[:, :groups] = np.where(fine, e + 127, 255)
     ok = fine[:, None, :, None]
     v = np.ldexp(np.where(ok, b, 0.0), -e[:, None, :, None])
-    codes = _nearest_code(np.abs(v)) + 128 * (np.signbit(b) & ok)
+    codes = _nearest_code(np.abs(v))
+    codes = np.where((codes == 0x78) & (e == 120)[:, None, :, None], 0x77, codes) + 128 * (np.signbit(b) & ok)
     return codes.astype(np.uint8).reshape(down * block_rows, groups * 128)[:rows], scales
 
 
