@@ -95,7 +95,7 @@ __device__ __forceinline__ Place place_of(long long base, unsigned per_row) {
 
 // Quantisation along the rows in blocks of 1 x 128.  A thread takes eight columns, 16
 // lanes a block, a wave the four groups of one scale word; F units a thread are read
-// together.  Bound by HBM: 8192 x 4096 bf16 in 20.6 us (4.9 TB/s), float32 31 us (5.4).
+// together.  Bound by HBM: 8192 x 4096 bf16 in 21 us (4.8 TB/s), float32 31 us (5.4).
 template <bool BF16, int F>
 __global__ __launch_bounds__(MX_THREADS) void fp8_rows(const void* x, long long ld, long long units, unsigned per_row,
                                                        long long cols, long long row_units, uint2* codes, unsigned* scales) {
@@ -141,8 +141,8 @@ __device__ __forceinline__ void put_scale(unsigned char* scales, long long row, 
 // column's eight codes of a lane go through LDS, at slots that keep the banks apart, and
 // leave 128 bytes a column.  Tiles go down four and along on an XCD, since neighbours
 // share lines of either form.  Bound by memory and by what registers leave of waves to wait
-// for it: 8192 x 4096 both forms bf16 33.5 us from HBM (4.0 TB/s) and 24.8 where the input is
-// in the last-level cache, float32 53.7 us; one form 22.6 and 41.8 us.
+// for it: 8192 x 4096 both forms bf16 33.8 us from HBM (4.0 TB/s) and 25 where the input is
+// in the last-level cache, float32 54 and 37 us; one form 24.5 and 43.6 us from HBM.
 template <bool BF16, bool ROWS, bool COLS, bool TILE>
 __global__ __launch_bounds__(MX_THREADS) void fp8_tiles(const void* x, long long ld, long long rows, long long cols, uint2* codes,
                                                         unsigned char* scales, uint2* codes_t, unsigned char* scales_t) {
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(MX_THREADS) void fp8_tiles(const void* x, long long
 
 // The values of a held matrix, exact in float32, rounded once to bf16 (half a step of bf16,
 // which is what was asked for).  A thread writes 16 bytes.  Bound by HBM: 8192 x 4096 to bf16 in
-// 17 us (5.9 TB/s), to float32 in 25 us (6.7).
+// 20.4 us (4.9 TB/s), to float32 in 35 us (4.8); 17 and 25 us where the codes are in the last-level cache.
 template <bool BF16>
 __global__ __launch_bounds__(MX_THREADS) void fp8_values(const unsigned char* codes, const unsigned char* scales, int shift,
                                                          long long scale_pitch, long long units, unsigned per_row, long long cols,
