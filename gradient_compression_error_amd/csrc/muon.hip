@@ -10,13 +10,17 @@
 // Numerics.  A step multiplies what it finds at small singular values by a (3.4), so a
 // rounding of the first step is 140 times as large after the fifth: products of bf16 or f16
 // operands alone are 0.003 to 0.15 off in the end.  So X, A and P are held as pairs of f16,
-// hi = fl16(v 2^e), lo = fl16(v 2^e - hi), 22 to 24 bits together, and a product is three
-// matrix instructions, hi hi + hi lo + lo hi, summed in float32: as good as float32
+// hi = fl16(v 2^e), lo = fl16((v 2^e - hi) low), 22 to 24 bits together, and a product is three
+// matrix instructions, hi hi + (hi lo + lo hi) / low, summed in float32: as good as float32
 // products for entries that are not small.  A bf16 result is the float32 one rounded once.
 // f16 has a least value, 2^-24, and so have the pairs.  Each step's powers of two (Step) are the
-// largest that keep hi below f16's largest value: with the usual coefficients X and A are off by
-// 2^-40 at most however small an entry is, and P by 2^-39; float32 has no such limit.  f16 subnormals
-// are kept by the matrix instructions.
+// largest that keep hi below f16's largest value, and with low = 2^11, which takes lo to hi's range,
+// X and A are off by 2^-51 at most however small an entry is with the usual coefficients, P by 2^-50:
+// half of the rows of 64 x 576 at 2^-24 of the others are 7e-7 off after five steps (float32 1e-7).
+// The small products want sums of their own then, which tiles of 192 and 256 have no registers for
+// (4096 x 4096: X X^T 200 us, with second sums 262, with a pass over k for them 239, by tiles of 128
+// 238; P X 340, 445 with such a pass, 352 by 128).  Sets that take those tiles have low = 1: 2^-40 and 2^-39.
+// f16 subnormals are kept by the matrix instructions.
 //
 // Layout.  A held matrix has rows of groups of 32 columns, 128 bytes each: 32 hi, then
 // 32 lo, zeros behind the last column.  X is held by rows (for A) and transposed (for P X), A
@@ -54,9 +58,9 @@ __host__ __device__ inline int mu_chunk(long long entries) {
 }
 __host__ __device__ inline int mu_sums(long long entries) { return static_cast<int>((entries + mu_chunk(entries) - 1) / mu_chunk(entries)); }
 
-// What a product's sums are multiplied by; for P also what A is, and what its diagonal gets.
+// What a product's sums are multiplied by; for P also what A is, and what its diagonal gets; what lo is held times.
 struct Factors {
-    float out, old, one;
+    float out, old, one, low;
 };
 
 // A call's matrices.  The first kernel gets the table as an argument and leaves it at the
@@ -77,15 +81,15 @@ static_assert(sizeof(Table) % 4 == 0 && sizeof(Table) <= 4096 - 64, "a launch's 
 constexpr int64_t SUMS_AT = (sizeof(Table) + 1023) / 1024 * 1024;   // the partial sums, behind the table
 constexpr int tile_kind(int kind) { return kind < APPLY ? kind : APPLY; }
 
-// Eight values as pairs: two conversions and a mixed subtraction for two of them.
+// Eight values as pairs: two conversions and a mixed subtraction (exact) for two of them.
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ f16x8 halves(const float (&v)[8], f16x8& lo) {
+__device__ __forceinline__ f16x8 halves(const float (&v)[8], float low, f16x8& lo) {
     f16x8 hi;
 #pragma unroll
     for (int q = 0; q < 8; q += 2) {
         const f16x2 h = __builtin_convertvector((f32x2{v[q], v[q + 1]}), f16x2);
-        const f16x2 l = __builtin_convertvector((f32x2{__builtin_fmaf(static_cast<float>(h[0]), -1.0f, v[q]),
-                                                       __builtin_fmaf(static_cast<float>(h[1]), -1.0f, v[q + 1])}), f16x2);
+        const f16x2 l = __builtin_convertvector((f32x2{low * __builtin_fmaf(static_cast<float>(h[0]), -1.0f, v[q]),
+                                                       low * __builtin_fmaf(static_cast<float>(h[1]), -1.0f, v[q + 1])}), f16x2);
         hi[q] = h[0]; hi[q + 1] = h[1];
         lo[q] = l[0]; lo[q + 1] = l[1];
     }
@@ -93,7 +97,7 @@ __device__ __forceinline__ f16x8 halves(const float (&v)[8], f16x8& lo) {
 }
 
 // Writes eight columns of a held row, `col` a multiple of 8; columns from `cols` on are zeros.
-__device__ __forceinline__ void put8(char* row, int col, int cols, float (&v)[8]) {
+__device__ __forceinline__ void put8(char* row, int col, int cols, float (&v)[8], float low) {
     if (col >= ((cols + 31) & ~31)) return;
     if (col + 8 > cols) {
 #pragma unroll
@@ -101,7 +105,7 @@ __device__ __forceinline__ void put8(char* row, int col, int cols, float (&v)[8]
             if (col + q >= cols) v[q] = 0.0f;
     }
     f16x8 lo;
-    const f16x8 hi = halves(v, lo);
+    const f16x8 hi = halves(v, low, lo);
     char* const to = row + (col >> 5) * 128ll + (col & 31) * 2;
     *reinterpret_cast<f16x8*>(to) = hi;
     *reinterpret_cast<f16x8*>(to + 64) = lo;
@@ -164,7 +168,7 @@ __global__ __launch_bounds__(256) void muon_moment(const Table table, float beta
 // stays zero; one with an entry that is not finite becomes NaN.  Bound by HBM: 12.6M float32
 // entries in 39 us (16 bytes each, 5.1 TB/s), the norm needed before any of it.
 template <bool BF16>
-__global__ __launch_bounds__(256) void muon_start(const Table* __restrict__ table, float beta, int nesterov, float sx, char* ws) {
+__global__ __launch_bounds__(256) void muon_start(const Table* __restrict__ table, float beta, int nesterov, float sx, float low, char* ws) {
     __shared__ float tile[64][65];
     __shared__ double sums[4];
     const int w = find_segment(table->start_at, table->count, blockIdx.x), t = blockIdx.x - table->start_at[w];
@@ -209,12 +213,12 @@ __global__ __launch_bounds__(256) void muon_start(const Table* __restrict__ tabl
         if (i0 + r < n) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = tile[r][c + q];
-            put8(by_rows + (i0 + r) * mu_groups(m) * 128, j0 + c, m, v);
+            put8(by_rows + (i0 + r) * mu_groups(m) * 128, j0 + c, m, v, low);
         }
         if (j0 + r < m) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = tile[c + q][r];
-            put8(by_cols + (j0 + r) * mu_groups(n) * 128, i0 + c, n, v);
+            put8(by_cols + (j0 + r) * mu_groups(n) * 128, i0 + c, n, v, low);
         }
     }
 }
@@ -295,6 +299,7 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
     const int lane = threadIdx.x & 63, rows = s.n, cols = symmetric(KIND) ? s.n : s.m;
     if (row0 >= rows || col0 >= cols) return;
     const float by = KIND == GRAM && b.part >= 0 ? 1.0f : f.out;
+    const float back = 1.0f / f.low;
     const float scale = LAST ? table->scale[b.w] : 1.0f;     // (not into `by`, which a small one would take below 2^-126)
     const bool turned = LAST && table->turned[b.w];
     if (!turned) {
@@ -343,7 +348,7 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
                 if constexpr (KIND == POLY) {                // c A^2 + b A + a I
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        v[q] += f.old * (static_cast<float>(old[p][0][q]) + static_cast<float>(old[p][1][q]));
+                        v[q] += f.old * __builtin_fmaf(static_cast<float>(old[p][1][q]), back, static_cast<float>(old[p][0][q]));
                         if (row == col + q) v[q] += f.one;
                     }
 #pragma unroll
@@ -351,7 +356,7 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
                         *reinterpret_cast<float4*>(region + r * COLS + ((c / 4 + q) ^ (r & 7)) * 4) =
                             make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 }
-                put8(ws + (KIND == GRAM ? at_a(s) : KIND == POLY ? at_p(s) : at_x(s)) + row * mu_groups(cols) * 128, col, cols, v);
+                put8(ws + (KIND == GRAM ? at_a(s) : KIND == POLY ? at_p(s) : at_x(s)) + row * mu_groups(cols) * 128, col, cols, v, f.low);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -385,7 +390,7 @@ __device__ __forceinline__ void emit(float* region, const Job& b, int row0, int 
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = factor * region[(k + q) * COLS + ((c >> 2) ^ (k + q & 7)) * 4 + (c & 3)];
-            if (col < cols) put8(to + col * pitch, row0 + k, s.n, v);
+            if (col < cols) put8(to + col * pitch, row0 + k, s.n, v, f.low);
         }
     }
 }
@@ -407,7 +412,7 @@ __device__ __forceinline__ void lay(float* region, int y, const f32x16& acc) {
 // holds a row's 128 bytes together, its eight pieces permuted so that a fragment's reads
 // meet no bank twice: piece b of row i of a fragment at slot b ^ (i >> 1 & 7).
 template <int BM, int BN, int WM, int WN, int RING, int KIND>
-__global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict__ table, char* ws, int turn, Factors f) {
+__global__ __launch_bounds__(WM* WN * 64, BM <= 128 ? 2 : 1) void muon_tile(const Table* __restrict__ table, char* ws, int turn, Factors f) {
     constexpr int NW = WM * WN, ROWS = BM + BN, MI = BM / WM / 32, NI = BN / WN / 32;
     constexpr int CP = ROWS / 8 / NW;                       // 8-row copies a wave makes for a group
     constexpr int GROUP = ROWS * 128;
@@ -451,9 +456,9 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
         }
     };
 
-    // A matrix instruction waits for the one before on the same sums: with few fragments the
-    // products hi hi, hi lo and lo hi have sums of their own.
-    constexpr int SETS = MI * NI < 4 ? 3 : 1;
+    // hi hi has sums of its own where registers allow (low may be anything then).  A matrix instruction
+    // waits for the one before on the same sums: with few fragments hi lo and lo hi are apart too.
+    constexpr int SETS = MI * NI < 4 ? 3 : MI * NI == 4 ? 2 : 1;
     f32x16 acc[SETS][MI][NI];
 #pragma unroll
     for (int e = 0; e < SETS; ++e)
@@ -494,7 +499,7 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
             const int x = t % MI, h = t / MI % 3, k = t / MI / 3, hl = h == 2, hr = h == 1;
 #pragma unroll
             for (int y = 0; y < NI; ++y) {
-                f32x16& sum = acc[SETS > 1 ? h : 0][x][y];
+                f32x16& sum = acc[min(h, SETS - 1)][x][y];
                 sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(r[k][y][hr], l[k][x][hl], sum, 0, 0, 0);
             }
             if constexpr (G == 1) {
@@ -528,12 +533,16 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
     constexpr int COLS = NI * 32;
     static_assert(NW * 32 * COLS * 4 <= RING * GROUP, "the results' regions must fit");
     float* const mine = reinterpret_cast<float*>(lds) + wave * 32 * COLS;
+    const float back = 1.0f / f.low;
 #pragma unroll
     for (int x = 0; x < MI; ++x) {
 #pragma unroll
         for (int y = 0; y < NI; ++y) {
+            if constexpr (SETS == 3) acc[1][x][y] += acc[2][x][y];
+            if constexpr (SETS > 1) {
 #pragma unroll
-            for (int e = SETS - 2; e >= 0; --e) acc[e][x][y] += acc[e + 1][x][y];   // the small ones first
+                for (int r = 0; r < 16; ++r) acc[0][x][y][r] = __builtin_fmaf(acc[1][x][y][r], back, acc[0][x][y][r]);
+            }
             lay<COLS>(mine, y, acc[0][x][y]);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -544,7 +553,7 @@ __global__ __launch_bounds__(WM* WN * 64) void muon_tile(const Table* __restrict
 
 // A from the parts of its k, added in order: 64 x 64 entries on or below the diagonal.  On it
 // the entries above are those below (the parts may not have them).
-__global__ __launch_bounds__(256) void muon_join(const Table* __restrict__ table, char* ws, float by) {
+__global__ __launch_bounds__(256) void muon_join(const Table* __restrict__ table, char* ws, float by, float low) {
     __shared__ float sums[64][65];
     const int w = find_segment(table->join_at, table->count, blockIdx.x);
     const Shape s = table->s[w];
@@ -579,12 +588,12 @@ __global__ __launch_bounds__(256) void muon_join(const Table* __restrict__ table
         if (i0 + r < s.n) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = I == J && c + q > r ? sums[c + q][r] : sums[r][c + q];
-            put8(to + (i0 + r) * pitch, j0 + c, s.n, v);
+            put8(to + (i0 + r) * pitch, j0 + c, s.n, v, low);
         }
         if (I != J && j0 + r < s.n) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = sums[c + q][r];
-            put8(to + (j0 + r) * pitch, i0 + c, s.n, v);
+            put8(to + (j0 + r) * pitch, i0 + c, s.n, v, low);
         }
     }
 }
@@ -684,6 +693,7 @@ void launch_product(Way way, unsigned grid, char* ws, int turn, const Factors& f
 int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float beta, int nesterov, int steps, const Step* step,
         char* ws, hipStream_t s) {
     const Cut cut = cut_of(mats, count);
+    const float low = cut.low();
     Table table;
     table.count = count;
     layout(mats, count, cut, table.s);
@@ -710,19 +720,20 @@ int run(const gc_muon_mat* mats, int count, int grad_dtype, int out_dtype, float
     }
     {
         TimedLaunch tl("muon_start", s);
-        if (grad_dtype == GC_BF16) muon_start<true><<<tiles, 256, 0, s>>>(held, beta, nesterov, step[0].sx, ws);
-        else muon_start<false><<<tiles, 256, 0, s>>>(held, beta, nesterov, step[0].sx, ws);
+        if (grad_dtype == GC_BF16) muon_start<true><<<tiles, 256, 0, s>>>(held, beta, nesterov, step[0].sx, low, ws);
+        else muon_start<false><<<tiles, 256, 0, s>>>(held, beta, nesterov, step[0].sx, low, ws);
     }
     int rc = check_launch("gc_muon_step");
     for (int k = 0; k < steps && rc == GC_OK; ++k) {
         const Step& t = step[k];
         const bool last = k + 1 == steps;
-        const Factors gram = {t.sa / (t.sx * t.sx), 0, 0}, poly = {t.c * (t.sp / (t.sa * t.sa)), t.b * (t.sp / t.sa), t.a * t.sp},
-                      apply = {(last ? 1.0f : step[k + 1].sx) / (t.sp * t.sx), 0, 0};
+        const Factors gram = {t.sa / (t.sx * t.sx), 0, 0, low},
+                      poly = {t.c * (t.sp / (t.sa * t.sa)), t.b * (t.sp / t.sa), t.a * t.sp, low},
+                      apply = {(last ? 1.0f : step[k + 1].sx) / (t.sp * t.sx), 0, 0, low};
         launch_product<GRAM>(cut.way[GRAM], grid[GRAM], ws, k & 1, gram, s);
         if (joins > 0) {
             TimedLaunch tl("muon_join", s);
-            muon_join<<<joins, 256, 0, s>>>(held, ws, gram.out);
+            muon_join<<<joins, 256, 0, s>>>(held, ws, gram.out, low);
         }
         launch_product<POLY>(cut.way[POLY], grid[POLY], ws, k & 1, poly, s);
         if (!last) launch_product<APPLY>(cut.way[APPLY], grid[APPLY], ws, k & 1, apply, s);

@@ -84,6 +84,8 @@ double time_of(int kind, Way way, const Shape* shapes, const int* per, int count
 struct Cut {
     Way way[3];                                              // A, P, P X
     int per[MU_MAX];
+    // what a pair's lo is held times: 1 where a tile has one set of sums for all products of a pair
+    float low() const { return std::max({way[GRAM], way[POLY], way[APPLY]}) < TILE_192 ? 2048.0f : 1.0f; }
 };
 Cut cut_of(const gc_muon_mat* mats, int count) {
     Shape shapes[MU_MAX];

@@ -543,12 +543,14 @@ size_t gc_muon_workspace_bytes(const gc_muon_mat* mats, int nmats);
  * matrix's), and within 2e-6 to 2e-5 for matrices whose singular values are not far
  * apart.  A bf16 out is the float32 one rounded once (1.7e-3).
  *   Pairs have a least value, which float32 has not: with the usual coefficients an entry
- * of X (the whole of which has norm 1 at first) or A is off by up to 2^-40 however
- * small it is, one of a + b A + c A A by 2^-39 (by up to 2^-38, 2^-36 and 2^-36 with others).
- * The matrix as a whole does not notice, but rows or columns much smaller than the
- * rest do: at 2^-12 of the others' size they are about as good as float32's, at 2^-16
- * they are off by 5e-6 (64 x 576) to 3e-5 (1024 x 1024) of their own size, at 2^-20 by 8e-5
- * to 4e-4, at 2^-24 by 1e-3 to 7e-3.
+ * of X (the whole of which has norm 1 at first) or A is off by up to 2^-51 however
+ * small it is, one of a + b A + c A A by 2^-50; by 2^-40 and 2^-39 in sets that take the
+ * largest tiles, which have no registers for more (some shapes past 1500 x 1500; with other
+ * coefficients by up to 16 times as much).  The matrix as a whole does not notice, but
+ * rows or columns much smaller than the rest do: at 2^-20 of the others' size they are
+ * as good as float32's, at 2^-24 off by 7e-7 (64 x 576) to 4e-6 (1024 x 1024) of
+ * their own size.  With the largest tiles (3010 x 2990) they are off by 5e-6 at 2^-12, 8e-5 at
+ * 2^-16, 1e-3 at 2^-20 and 2e-2 at 2^-24.
  * How sums are cut follows from the shapes of the whole set, so a matrix may have
  * other last bits in another set.
  * Kernel launches only: no copy, no allocation, no synchronisation, so the call may

@@ -35,7 +35,7 @@ int main() {
         for (auto& a : mats)
             if (scanf("%d %d", &a.n, &a.m) != 2) return 1;
         const Cut cut = cut_of(mats.data(), count);
-        printf("%s %s %s", names[cut.way[GRAM]], names[cut.way[POLY]], names[cut.way[APPLY]]);
+        printf("%d %s %s %s", static_cast<int>(cut.low()), names[cut.way[GRAM]], names[cut.way[POLY]], names[cut.way[APPLY]]);
         for (int w = 0; w < count; ++w) printf(" %d", static_cast<int>(parts_of(oriented(mats[w]), cut.per[w])));
         printf("\n");
     }
@@ -65,5 +65,13 @@ def fp8_plans(shapes):
 
 def muon_cuts(sets):
     """[[(n, m), ...] of at most 32] -> [((tile of X X^T, of P, of P X), [parts of k of each matrix])]."""
-    got = _asked(MUON, [f"{len(s)} " + " ".join(f"{n} {m}" for n, m in s) for s in sets])
-    return [(tuple(g[:3]), [int(v) for v in g[3:]]) for g in got]
+    return [(tuple(g[1:4]), [int(v) for v in g[4:]]) for g in _muon(sets)]
+
+
+def muon_lows(sets):
+    """What a pair's lo is held times, for each set."""
+    return [int(g[0]) for g in _muon(sets)]
+
+
+def _muon(sets):
+    return _asked(MUON, [f"{len(s)} " + " ".join(f"{n} {m}" for n, m in s) for s in sets])

@@ -4,7 +4,7 @@ import os
 import re
 
 from gradient_compression_error_amd import build
-from plan_util import FP8, MUON, fp8_plans, muon_cuts
+from plan_util import FP8, MUON, fp8_plans, muon_cuts, muon_lows
 from test_gpu_fp8_kernels import LARGE, SHAPES
 from test_gpu_muon_kernels import SETS
 
@@ -66,6 +66,9 @@ def test_muon_kernels_are_reached():
     gram, poly, apply = muon_reached(SETS)
     assert gram == {(w, parts) for w in small for parts in (False, True)}
     assert poly == small and apply == small | {"TILE_256"}
+    # pairs of either kind; what test_gpu_muon_accuracy says of its shapes
+    assert set(muon_lows(SETS)) == {1, 2048}
+    assert muon_lows([[s] for s in [(64, 576), (576, 64), (33, 31), (130, 257), (300, 1111), (1500, 1400), (3010, 2990)]]) == [2048] * 6 + [1]
     # a layer's set: the long matrices' X X^T in parts on the paired tile, the square ones' whole
     assert muon_cuts(SETS[:1])[0][0][0] == "TILE_128_PAIRED" and muon_cuts(SETS[:1])[0][1] == [1, 1, 1, 1, 4, 4]
 
