@@ -28,7 +28,7 @@
 //
 // Bounds, five steps to bf16: large matrices by the matrix units at the clock that power
 // leaves (4096 x 4096 3.5 to 3.6 ms, 1.2 PFLOP/s of f16, units busy 61 to 74% of the cycles); a
-// set of middling ones by rounds of tiles (a width-1024 layer's six 0.84 to 0.89 ms, units busy 27 to
+// set of middling ones by rounds of tiles (a width-1024 layer's six 0.84 to 0.91 ms, units busy 27 to
 // 53%); small ones by 17 to 22 dependent launches of 4 to 7 us (64 x 576 82 us).  Results in float32
 // take as long.
 #include <algorithm>
