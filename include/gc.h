@@ -538,19 +538,20 @@ size_t gc_muon_workspace_bytes(const gc_muon_mat* mats, int nmats);
  *   ws       >= gc_muon_workspace_bytes(mats, nmats) bytes
  * Sums are in float32 (the norm's in float64); X, A and a + b A + c A A are held as
  * pairs of 11-bit floating point numbers, 22 to 24 bits together, and rounded once to
- * out.  The usual coefficients make what a step rounds up to 3.4 times as large with every step
- * that follows: a float32 out is within about 2e-4 of the exact one (2-norm over the
- * matrix's), and within 2e-6 to 2e-5 for matrices whose singular values are not far
- * apart.  A bf16 out is the float32 one rounded once (1.7e-3).
- *   Pairs have a least value, which float32 has not: with the usual coefficients an entry
- * of X (the whole of which has norm 1 at first) or A is off by up to 2^-51 however
- * small it is, one of a + b A + c A A by 2^-50; by 2^-40 and 2^-39 in sets that take the
- * largest tiles, which have no registers for more (some shapes past 1500 x 1500; with other
- * coefficients by up to 16 times as much).  The matrix as a whole does not notice, but
- * rows or columns much smaller than the rest do: at 2^-20 of the others' size they are
- * as good as float32's, at 2^-24 off by 7e-7 (64 x 576) to 4e-6 (1024 x 1024) of
- * their own size.  With the largest tiles (3010 x 2990) they are off by 5e-6 at 2^-12, 8e-5 at
- * 2^-16, 1e-3 at 2^-20 and 2e-2 at 2^-24.
+ * out.  The usual coefficients make what a step rounds up to 3.4 times as large with
+ * every step that follows: a float32 out is within about 2e-4 of the exact one (2-norm
+ * over the matrix's), and within 2e-6 to 2e-5 for matrices whose singular values are not
+ * far apart.  A bf16 out is the float32 one rounded once (1.7e-3).
+ *   Pairs have a least value, which float32 has not: with the usual coefficients an
+ * entry of X (the whole of which has norm 1 at first) or A is off by up to 2^-51
+ * however small it is, one of a + b A + c A A by 2^-50; by 2^-40 and 2^-39 in sets that
+ * take the largest tiles, which have no registers for more (single matrices from about
+ * 2000 x 2000 or 1500 x 6000 on, sets of sixteen from about 900 x 900 on; which ones, follows
+ * from the shapes); with other coefficients by up to 16 times as much.  The matrix as
+ * a whole does not notice, but rows or columns much smaller than the rest do: at 2^-20
+ * of the others' size they are as good as float32's, at 2^-24 off by 7e-7 (64 x 576) to
+ * 4e-6 (1024 x 1024) of their own size.  With the largest tiles (3010 x 2990) they are
+ * off by 5e-6 at 2^-12, 8e-5 at 2^-16, 1e-3 at 2^-20 and 2e-2 at 2^-24.
  * How sums are cut follows from the shapes of the whole set, so a matrix may have
  * other last bits in another set.
  * Kernel launches only: no copy, no allocation, no synchronisation, so the call may
